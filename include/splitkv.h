@@ -58,6 +58,10 @@ extern "C" {
 #define SPLITKV_DEV_BAD_PLAN 0x8     /* a queue entry or item id out of range                      */
 #define SPLITKV_DEV_TIMEOUT 0x10     /* an in-kernel wait passed its time limit; the kernel returned */
 #define SPLITKV_DEV_SMEM_ALIGN 0x20  /* dynamic shared memory not 1024-byte aligned; the backward returned */
+#define SPLITKV_DEV_BAD_PAGE 0x40    /* paged: a page in use outside [0, n_pages), or a selection out of order  */
+#define SPLITKV_DEV_BAD_LENGTH 0x80  /* paged: a sequence length outside [0, max_pages * page_size]          */
+#define SPLITKV_DEV_BAD_TOKEN 0x100  /* paged: a token's sequence or position out of range                   */
+#define SPLITKV_DEV_TOKEN_ORDER 0x200 /* paged: tokens not strictly ascending by (sequence, position)        */
 
 /* Element types of q, k, v, kb, vb, o, dout. Accumulation is always float32. */
 #define SPLITKV_F32 0
@@ -328,6 +332,113 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
                           const int32_t *anchors_d, const int32_t *chunk_rank_d, int32_t rank, int32_t n_ranks,
                           float *dq, float *dk, float *dv, float *dkb, float *dvb, int32_t *status_d,
                           void *workspace_d, size_t workspace_bytes, void *stream);
+
+/*
+ * ---- Paged key-value cache: serving one token at a time ----
+ *
+ * The calls above attend whole draft blocks to a packed context. The calls below serve a model whose
+ * context grows token by token and lies in pages of a cache: splitkv_paged_append writes new tokens'
+ * keys and values (rotary positions applied on the way), splitkv_paged_decode attends one new token
+ * of each sequence to the sequence's cached keys (split over its length, the parts joined by the same
+ * log-sum-exp merge), and splitkv_paged_select picks, for each token and kv head, the pages that a
+ * cheap score ranks highest, so that splitkv_paged_decode reads those pages only.
+ *
+ *   k_cache, v_cache  element (page, g, t, i) of page `page`, kv head g, position t within the page and
+ *                     channel i at page*page_stride + g*head_stride + t*token_stride + i (elements):
+ *                     any order of the three outer dimensions, no two of them overlapping.
+ *   k_bounds          [n_pages, Hkv, 2, d], dense, the problem's dtype: the smallest and the largest
+ *                     value of each channel over the page's keys (as the cache holds them).
+ *   page_table_d      int32, row b (table_stride entries apart) lists the cache pages of sequence b: its
+ *                     position p lies in page row[p / page_size] at offset p % page_size. Entries past
+ *                     a sequence's length are not read. Two sequences may share pages (a common
+ *                     prefix); to attend several new tokens of one sequence, list its row several
+ *                     times with the lengths that each of them sees.
+ *   q, o              [n_seqs, Hq, d]; q's tokens are q_stride elements apart (a slice of a fused
+ *                     projection), each token's heads dense; o and lse [n_seqs, Hq] are dense.
+ * Pointers are 16-byte aligned and every stride a multiple of 16 bytes. Sums, maxima and partial
+ * results are float32; scores that choose pages are float64, so that no rounding decides a choice.
+ * Lengths, tables and token lists are device data, read by the kernels only: a call captured into a
+ * CUDA graph follows their values at each replay. What only the device can see (lengths, pages and
+ * tokens out of range) is ORed into status_d; the results of that call are then unspecified, but
+ * nothing outside the given buffers is read or written.
+ */
+
+/* Most sequences one call may hold, and most pages of a sequence that splitkv_paged_select ranks. */
+#define SPLITKV_PAGED_MAX_SEQS 4096
+#define SPLITKV_PAGED_MAX_SELECT_PAGES 131072
+
+typedef struct {
+    int32_t n_q_heads;    /* Hq                                                                   */
+    int32_t n_kv_heads;   /* Hkv, divides Hq                                                      */
+    int32_t head_dim;     /* d: bf16 a multiple of 8, f32 a multiple of 4; 8..128                 */
+    int32_t page_size;    /* positions per page: a power of two, 1..1024                          */
+    int64_t n_pages;      /* pages of the cache                                                   */
+    int32_t max_pages;    /* entries of a page-table row: the longest sequence is max_pages pages */
+    int64_t table_stride; /* entries from one row of the page table to the next, >= max_pages     */
+    int64_t page_stride;  /* strides of k_cache and v_cache, in elements                          */
+    int64_t head_stride;
+    int64_t token_stride;
+    float scale;          /* score scale, normally 1/sqrt(d)                                      */
+    int32_t dtype;        /* SPLITKV_F32 or SPLITKV_BF16                                          */
+} splitkv_paged;
+
+/* Bytes of scratch that splitkv_paged_decode needs for up to n_seqs sequences (0 on a bad description; the
+ * same on every device). The caller zeroes the buffer once, before its first
+ * use; each call leaves it ready for the next. Calls that share a buffer must be ordered (one stream, or
+ * events): a captured graph that may run beside other work needs a buffer of its own. */
+size_t splitkv_paged_workspace_size(const splitkv_paged *paged, int32_t n_seqs);
+
+/*
+ * Append: for each token i < n_tokens with token_seq_d[i] = b >= 0 and token_pos_d[i] = p, rotates its keys
+ * and writes them and its values to position p of sequence b. token_seq_d[i] < 0 marks padding: nothing is
+ * written to the cache. The other tokens must be strictly ascending by (b, p) (SPLITKV_DEV_TOKEN_ORDER):
+ * no position is given twice.
+ *   k, v   [n_tokens, Hkv, d], tokens k_stride and v_stride elements apart, each token's heads dense.
+ *   q      [n_tokens, Hq, d] (q_stride) or NULL: rotated into q_out [n_tokens, Hq, d] (dense, apart from
+ *          q). A padding token's queries are copied as they are.
+ *   rope   float32 [rope_len, rope_dim], or NULL (no rotation; rope_dim = 0): row p holds rope_dim/2 cosines
+ *          and then rope_dim/2 sines for position p. Channel pairs (i, i + rope_dim/2), or (2i, 2i+1) with
+ *          interleaved != 0, turn by angle i: (x c - y s, y c + x s), in float32, rounded once; channels
+ *          from rope_dim on are copied. rope_dim is even, at most d.
+ *   k_bounds  or NULL: for every page written, the bounds of the keys at its positions 0 .. the last one
+ *          written by this call (positions before the new ones are read from the cache; what lies behind
+ *          counts as absent, so a sequence that was cut back is followed). A NaN key value is passed over.
+ */
+int splitkv_paged_append(const splitkv_paged *paged, int32_t n_seqs, int64_t n_tokens, const void *q, int64_t q_stride,
+                         const void *k, int64_t k_stride, const void *v, int64_t v_stride, const float *rope,
+                         int32_t rope_dim, int64_t rope_len, int32_t interleaved, const int32_t *page_table_d,
+                         const int32_t *token_seq_d, const int32_t *token_pos_d, void *q_out, void *k_cache,
+                         void *v_cache, void *k_bounds, int32_t *status_d, void *stream);
+
+/*
+ * Decode attention: for each sequence b and query head h (kv head g = h / (Hq/Hkv)), over the cached keys
+ * j < seq_len_d[b]:
+ *   s_j = scale * q_bh . k_j,  lse_bh = log sum_j exp(s_j) (natural log),  o_bh = sum_j exp(s_j - lse_bh) v_j
+ * A row without keys (length 0, or only scores of -inf) gets o = 0, lse = -inf. Cache positions at or past
+ * the length are not read. pages_d NULL: every key. Otherwise pages_d [n_seqs, Hkv, n_select] lists the page-table
+ * entries (page p: positions p*page_size ..) to read for (b, g): strictly ascending, within the sequence's
+ * pages, the unused tail filled with -1 (anything else: SPLITKV_DEV_BAD_PAGE).
+ */
+int splitkv_paged_decode(const splitkv_paged *paged, int32_t n_seqs, const void *q, int64_t q_stride,
+                         const void *k_cache, const void *v_cache, const int32_t *page_table_d,
+                         const int32_t *seq_len_d, const int32_t *pages_d, int32_t n_select, void *o, float *lse,
+                         int32_t *status_d, void *workspace_d, size_t workspace_bytes, void *stream);
+
+/*
+ * Page selection: for each sequence b and kv head g, with a_i = sum_h max(q_bhi, 0) and b_i = sum_h min(q_bhi, 0)
+ * over the query heads h of g, page p scores
+ *   sum_i a_i kmax_pi + b_i kmin_pi = sum_h sum_i max(q_bhi kmin_pi, q_bhi kmax_pi),
+ * which no key of the page exceeds in sum_h q_bh . k. pages_d [n_seqs, Hkv, n_select] receives the n_select pages
+ * to read, in ascending order, then -1: the first keep_first and the last keep_last pages of the sequence, then
+ * those with the highest scores; equal scores go to the lower page. The sum is formed as on the left, in float64: a
+ * bound that is infinite or NaN (0 * inf) may make it NaN, which counts as the lowest score. The first
+ * pages go before the last ones where n_select does not hold both. max_pages is at most
+ * SPLITKV_PAGED_MAX_SELECT_PAGES (EUNSUPPORTED beyond).
+ */
+int splitkv_paged_select(const splitkv_paged *paged, int32_t n_seqs, const void *q, int64_t q_stride,
+                         const void *k_bounds, const int32_t *page_table_d, const int32_t *seq_len_d,
+                         int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t *pages_d,
+                         int32_t *status_d, void *stream);
 
 #ifdef __cplusplus
 }

@@ -18,9 +18,11 @@ _lib = ctypes.CDLL(LIB_PATH)
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOSPACE = 0, -1, -2, -3, -4
 DEV_ANCHOR_ORDER, DEV_ANCHOR_RANGE, DEV_BAD_COST, DEV_BAD_PLAN, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
 DEV_SMEM_ALIGN = 0x20
+DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_BAD_TOKEN, DEV_TOKEN_ORDER = 0x40, 0x80, 0x100, 0x200
 F32, BF16 = 0, 1
 FWD_DEFAULT, FWD_SIMT, FWD_TEST_STARVE = 0, 1, 0x100
 MAX_BATCH = 64
+PAGED_MAX_SEQS, PAGED_MAX_SELECT_PAGES = 4096, 131072
 
 _i32, _i64, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -59,7 +61,25 @@ class Sizes(ctypes.Structure):
     ]
 
 
+class Paged(ctypes.Structure):
+    _fields_ = [
+        ("n_q_heads", _i32),
+        ("n_kv_heads", _i32),
+        ("head_dim", _i32),
+        ("page_size", _i32),
+        ("n_pages", _i64),
+        ("max_pages", _i32),
+        ("table_stride", _i64),
+        ("page_stride", _i64),
+        ("head_stride", _i64),
+        ("token_stride", _i64),
+        ("scale", _f32),
+        ("dtype", _i32),
+    ]
+
+
 _PP = ctypes.POINTER(Problem)
+_PG = ctypes.POINTER(Paged)
 _SIGS = {
     "splitkv_query": (_i32, [_PP, ctypes.POINTER(Sizes)]),
     "splitkv_workspace_size": (_sz, [_PP, _i32]),
@@ -79,6 +99,12 @@ _SIGS = {
     "splitkv_cost_rank": (_i32, [_PP, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "splitkv_lse_merge_rank": (_i32, [_PP, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp]),
     "splitkv_lse_merge_ranks": (_i32, [_PP, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "splitkv_paged_workspace_size": (_sz, [_PG, _i32]),
+    "splitkv_paged_append": (_i32, [_PG, _i32, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _i32]
+                             + [_vp] * 9),
+    "splitkv_paged_decode": (_i32, [_PG, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz,
+                                    _vp]),
+    "splitkv_paged_select": (_i32, [_PG, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
 }
 EXPORTS = tuple(_SIGS)
 for _name, (_res, _args) in _SIGS.items():
@@ -267,6 +293,47 @@ def splitkv_lse_merge_rank(problem, o_part, lse_part, anchors, chunk_rank, rank,
 def splitkv_lse_merge_ranks(problem, n_ranks, o_ranks, lse_ranks, o, lse, status, stream=None):
     _check(_lib.splitkv_lse_merge_ranks(problem.ptr, int(n_ranks), _p(o_ranks), _p(lse_ranks), _p(o), _p(lse),
                                         _p(status), _stream(stream)), "splitkv_lse_merge_ranks")
+
+
+def make_paged(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, strides, table_stride=None, scale=None,
+               dtype=torch.bfloat16) -> Paged:
+    """A ``splitkv_paged``; ``strides``: the caches' (page, kv head, position) strides in elements."""
+    code = F32 if dtype == torch.float32 else BF16 if dtype == torch.bfloat16 else None
+    if code is None:
+        raise SplitKVError(EUNSUPPORTED, f"dtype {dtype}")
+    scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
+    return Paged(int(n_q_heads), int(n_kv_heads), int(head_dim), int(page_size), int(n_pages), int(max_pages),
+                 int(max_pages if table_stride is None else table_stride), int(strides[0]), int(strides[1]),
+                 int(strides[2]), float(scale), code)
+
+
+def splitkv_paged_workspace_size(paged: Paged, n_seqs: int) -> int:
+    return int(_lib.splitkv_paged_workspace_size(ctypes.byref(paged), int(n_seqs)))
+
+
+def splitkv_paged_append(paged, n_seqs, n_tokens, q, q_stride, k, k_stride, v, v_stride, rope, rope_dim, rope_len,
+                         interleaved, page_table, token_seq, token_pos, q_out, k_cache, v_cache, k_bounds, status,
+                         stream=None):
+    _check(_lib.splitkv_paged_append(ctypes.byref(paged), int(n_seqs), int(n_tokens), _p(q), int(q_stride), _p(k),
+                                     int(k_stride), _p(v), int(v_stride), _p(rope), int(rope_dim), int(rope_len),
+                                     int(interleaved), _p(page_table), _p(token_seq), _p(token_pos), _p(q_out),
+                                     _p(k_cache), _p(v_cache), _p(k_bounds), _p(status), _stream(stream)),
+           "splitkv_paged_append")
+
+
+def splitkv_paged_decode(paged, n_seqs, q, q_stride, k_cache, v_cache, page_table, seq_len, pages, n_select, o, lse,
+                         status, workspace, stream=None):
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.splitkv_paged_decode(ctypes.byref(paged), int(n_seqs), _p(q), int(q_stride), _p(k_cache), _p(v_cache),
+                                     _p(page_table), _p(seq_len), _p(pages), int(n_select), _p(o), _p(lse), _p(status),
+                                     _p(workspace), nbytes, _stream(stream)), "splitkv_paged_decode")
+
+
+def splitkv_paged_select(paged, n_seqs, q, q_stride, k_bounds, page_table, seq_len, n_select, keep_first, keep_last,
+                         pages, status, stream=None):
+    _check(_lib.splitkv_paged_select(ctypes.byref(paged), int(n_seqs), _p(q), int(q_stride), _p(k_bounds),
+                                     _p(page_table), _p(seq_len), int(n_select), int(keep_first), int(keep_last),
+                                     _p(pages), _p(status), _stream(stream)), "splitkv_paged_select")
 
 
 # ------------------------------------------------------------------ convenience: the whole path

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 #define SPLITKV_API extern "C" __attribute__((visibility("default")))
 
@@ -403,4 +404,137 @@ SPLITKV_API int splitkv_attn_bwd_rank(const splitkv_problem* problem, const void
     if (rc) return rc;
     return attn_bwd(m, q, k, v, kb, vb, o, lse, dout, anchors_d, dq, dk, dv, dkb, dvb, status_d, workspace_d,
                     workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ paged cache
+namespace {
+
+// Fill `m` from a host description and a number of sequences; returns SPLITKV_OK or a negative code.
+int build_paged(const splitkv_paged* p, int64_t n_seqs, PagedMeta* m) {
+    if (!p) return SPLITKV_EINVAL;
+    if (p->n_q_heads < 1 || p->n_kv_heads < 1 || p->n_q_heads % p->n_kv_heads || p->head_dim < 1) return SPLITKV_EINVAL;
+    if (p->page_size < 1 || p->n_pages < 1 || p->max_pages < 1 || p->table_stride < p->max_pages) return SPLITKV_EINVAL;
+    if (n_seqs < 0) return SPLITKV_EINVAL;
+    if (!(p->scale > 0.f) || p->scale != p->scale || p->scale > 3.0e38f) return SPLITKV_EINVAL;
+    if (p->dtype != SPLITKV_F32 && p->dtype != SPLITKV_BF16) return SPLITKV_EUNSUPPORTED;
+    const int32_t vec = p->dtype == SPLITKV_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (p->head_dim % vec || p->head_dim > 128 || p->head_dim < 8) return SPLITKV_EUNSUPPORTED;
+    if (p->page_size > 1024 || (p->page_size & (p->page_size - 1))) return SPLITKV_EUNSUPPORTED;
+    if (p->n_pages > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX) return SPLITKV_EUNSUPPORTED;
+    if (n_seqs > SPLITKV_PAGED_MAX_SEQS || p->n_q_heads > 32768) return SPLITKV_EUNSUPPORTED;
+    // The units of work (16 positions of a sequence and kv head) are counted in 64 bits, those of one head in 32.
+    if (n_seqs * (((int64_t)p->max_pages * p->page_size + 15) / 16) > INT32_MAX) return SPLITKV_EUNSUPPORTED;
+    if (p->page_stride % vec || p->head_stride % vec || p->token_stride % vec) return SPLITKV_EINVAL;
+    // No two rows of the cache may overlap: by ascending stride, each step goes past what the smaller ones cover.
+    std::pair<int64_t, int64_t> dim[3] = {
+        {p->page_stride, p->n_pages}, {p->head_stride, p->n_kv_heads}, {p->token_stride, p->page_size}};
+    std::sort(dim, dim + 3);
+    int64_t covered = p->head_dim;
+    for (const auto& x : dim) {
+        if (x.second == 1) continue;
+        if (x.first < covered) return SPLITKV_EINVAL;
+        if (x.first > (int64_t)1 << 40) return SPLITKV_EUNSUPPORTED;
+        covered += (x.second - 1) * x.first;
+    }
+    m->hq = p->n_q_heads;
+    m->hkv = p->n_kv_heads;
+    m->group = p->n_q_heads / p->n_kv_heads;
+    m->d = p->head_dim;
+    m->page = p->page_size;
+    m->page_shift = __builtin_ctz((unsigned)p->page_size);
+    m->max_pages = p->max_pages;
+    m->n_seqs = (int32_t)n_seqs;
+    m->n_pages = p->n_pages;
+    m->table_stride = p->table_stride;
+    m->page_stride = p->n_pages > 1 ? p->page_stride : 0;
+    m->head_stride = p->n_kv_heads > 1 ? p->head_stride : 0;
+    m->token_stride = p->page_size > 1 ? p->token_stride : 0;
+    m->scale = p->scale;
+    m->dtype = p->dtype;
+    return SPLITKV_OK;
+}
+
+// A [n, heads, d] tensor of an append or decode call: 16-byte aligned rows, tokens that do not overlap.
+bool rows_ok(const PagedMeta& m, const void* x, int64_t n, int64_t stride, int32_t heads) {
+    const int32_t vec = m.dtype == SPLITKV_BF16 ? 8 : 4;
+    return x && aligned16(x) && (n <= 1 || (stride >= (int64_t)heads * m.d && stride % vec == 0 && stride <= (int64_t)1 << 32));
+}
+
+}  // namespace
+
+SPLITKV_API size_t splitkv_paged_workspace_size(const splitkv_paged* paged, int32_t n_seqs) {
+    PagedMeta m;
+    return build_paged(paged, n_seqs, &m) ? 0 : paged_decode_workspace(m);
+}
+
+SPLITKV_API int splitkv_paged_append(const splitkv_paged* paged, int32_t n_seqs, int64_t n_tokens, const void* q,
+                                     int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                     const float* rope, int32_t rope_dim, int64_t rope_len, int32_t interleaved,
+                                     const int32_t* page_table_d, const int32_t* token_seq_d,
+                                     const int32_t* token_pos_d, void* q_out, void* k_cache, void* v_cache,
+                                     void* k_bounds, int32_t* status_d, void* stream) {
+    clear_error();
+    PagedMeta m;
+    int rc = build_paged(paged, n_seqs, &m);
+    if (rc) return rc;
+    if (n_tokens < 0) return SPLITKV_EINVAL;
+    if (n_tokens > ((int64_t)1 << 30)) return SPLITKV_EUNSUPPORTED;
+    if (rope ? rope_dim < 2 || rope_dim % 2 || rope_dim > m.d || rope_len < 1 : rope_dim != 0) return SPLITKV_EINVAL;
+    if (!status_d) return SPLITKV_EINVAL;
+    if (n_tokens == 0) return SPLITKV_OK;
+    if (!rows_ok(m, k, n_tokens, k_stride, m.hkv) || !rows_ok(m, v, n_tokens, v_stride, m.hkv)) return SPLITKV_EINVAL;
+    if (q && (!rows_ok(m, q, n_tokens, q_stride, m.hq) || !q_out || !aligned16(q_out))) return SPLITKV_EINVAL;
+    if (!page_table_d || !token_seq_d || !token_pos_d || !k_cache || !v_cache) return SPLITKV_EINVAL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_bounds) || !aligned16(rope)) return SPLITKV_EINVAL;
+    if (q) {  // q_out is written while other blocks still read q
+        const int64_t e = m.dtype == SPLITKV_BF16 ? 2 : 4, row = (int64_t)m.hq * m.d * e;
+        const char *x = (const char*)q, *y = (const char*)q_out;
+        if (x < y + n_tokens * row && y < x + (n_tokens - 1) * q_stride * e + row) {
+            // A fused projection's rows may enclose the output's only if they are apart in memory: refuse any overlap.
+            return SPLITKV_EINVAL;
+        }
+    }
+    const AppendArgs a{n_tokens, q,           k,          v,           q_stride,    k_stride, v_stride,
+                       rope,     rope_dim,    interleaved, rope_len,   page_table_d, token_seq_d, token_pos_d,
+                       q_out,    k_cache,     v_cache,     k_bounds};
+    return cuda_status(launch_paged_append(m, a, status_d, (cudaStream_t)stream));
+}
+
+SPLITKV_API int splitkv_paged_decode(const splitkv_paged* paged, int32_t n_seqs, const void* q, int64_t q_stride,
+                                     const void* k_cache, const void* v_cache, const int32_t* page_table_d,
+                                     const int32_t* seq_len_d, const int32_t* pages_d, int32_t n_select, void* o,
+                                     float* lse, int32_t* status_d, void* workspace_d, size_t workspace_bytes,
+                                     void* stream) {
+    clear_error();
+    PagedMeta m;
+    int rc = build_paged(paged, n_seqs, &m);
+    if (rc) return rc;
+    if (!status_d || (pages_d && n_select < 1)) return SPLITKV_EINVAL;
+    if (n_seqs == 0) return SPLITKV_OK;
+    if (!rows_ok(m, q, n_seqs, q_stride, m.hq) || !k_cache || !v_cache || !page_table_d || !seq_len_d || !o || !lse)
+        return SPLITKV_EINVAL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return SPLITKV_EINVAL;
+    if (!workspace_d || workspace_bytes < paged_decode_workspace(m)) return SPLITKV_ENOSPACE;
+    if (!aligned16(workspace_d)) return SPLITKV_EINVAL;
+    return cuda_status(launch_paged_decode(m, q, q_stride, k_cache, v_cache, page_table_d, seq_len_d, pages_d,
+                                           pages_d ? n_select : 0, o, lse, status_d, workspace_d,
+                                           (cudaStream_t)stream));
+}
+
+SPLITKV_API int splitkv_paged_select(const splitkv_paged* paged, int32_t n_seqs, const void* q, int64_t q_stride,
+                                     const void* k_bounds, const int32_t* page_table_d, const int32_t* seq_len_d,
+                                     int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t* pages_d,
+                                     int32_t* status_d, void* stream) {
+    clear_error();
+    PagedMeta m;
+    int rc = build_paged(paged, n_seqs, &m);
+    if (rc) return rc;
+    if (!status_d || n_select < 1 || keep_first < 0 || keep_last < 0) return SPLITKV_EINVAL;
+    if (m.max_pages > kMaxSelectPages || n_select > kMaxSelectPages) return SPLITKV_EUNSUPPORTED;
+    if (n_seqs == 0) return SPLITKV_OK;
+    if (!rows_ok(m, q, n_seqs, q_stride, m.hq) || !k_bounds || !page_table_d || !seq_len_d || !pages_d)
+        return SPLITKV_EINVAL;
+    if (!aligned16(k_bounds)) return SPLITKV_EINVAL;
+    return cuda_status(launch_paged_select(m, q, q_stride, k_bounds, page_table_d, seq_len_d, n_select, keep_first,
+                                           keep_last, pages_d, status_d, (cudaStream_t)stream));
 }

@@ -1,0 +1,77 @@
+// Shared definitions of the paged-cache operators (append, one-token decode attention, page selection): the cache's
+// geometry by value, row addressing and the internal launcher declarations.
+#pragma once
+
+#include "common.cuh"
+
+namespace splitkv {
+
+// Geometry of a paged cache, by value. Strides in elements; page_size is a power of two.
+struct PagedMeta {
+    int32_t hq, hkv, group, d;
+    int32_t page, page_shift;   // positions per page, log2 of it
+    int32_t max_pages;          // entries of a page-table row that may be read
+    int32_t n_seqs;
+    int64_t n_pages;            // pages of the cache
+    int64_t table_stride;
+    int64_t page_stride, head_stride, token_stride;
+    float scale;
+    int32_t dtype;
+};
+
+// The tokens of one append call.
+struct AppendArgs {
+    int64_t n_tokens;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements from one token's first row to the next token's
+    const float* rope;                     // [rope_len][rope_dim]: rope_dim/2 cosines, then rope_dim/2 sines; or null
+    int32_t rope_dim, interleaved;
+    int64_t rope_len;
+    const int32_t *table, *token_seq, *token_pos;
+    void *q_out, *k_cache, *v_cache, *k_bounds;
+};
+
+// A token's place in the cache. page < 0: not to be written (padding, or a reason already in the status word).
+struct TokenPlace {
+    int32_t seq, pos;
+    int64_t page;
+};
+
+cudaError_t launch_paged_append(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st);
+
+cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,
+                                const void* v_cache, const int32_t* table, const int32_t* seq_len,
+                                const int32_t* pages, int32_t n_select, void* o, float* lse, int32_t* status, void* ws,
+                                cudaStream_t st);
+size_t paged_decode_workspace(const PagedMeta& m);
+
+cudaError_t launch_paged_select(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_bounds,
+                                const int32_t* table, const int32_t* seq_len, int32_t n_select, int32_t keep_first,
+                                int32_t keep_last, int32_t* pages, int32_t* status, cudaStream_t st);
+constexpr int32_t kMaxSelectPages = SPLITKV_PAGED_MAX_SELECT_PAGES;
+
+// Length of sequence b, or 0 (with the status bit) when it is not in [0, max_pages * page].
+__device__ __forceinline__ int32_t paged_len(const PagedMeta& m, const int32_t* seq_len, int32_t b, int32_t* status) {
+    const int32_t n = __ldg(seq_len + b);
+    if (n < 0 || n > (int64_t)m.max_pages * m.page) {
+        raise_status(status, SPLITKV_DEV_BAD_LENGTH);
+        return 0;
+    }
+    return n;
+}
+
+// Cache page behind entry `e` of a page-table row, or -1 (with the status bit) when it is out of range.
+__device__ __forceinline__ int32_t paged_page(const PagedMeta& m, const int32_t* row, int32_t e, int32_t* status) {
+    const int32_t p = __ldg(row + e);
+    if (p < 0 || p >= m.n_pages) {
+        raise_status(status, SPLITKV_DEV_BAD_PAGE);
+        return -1;
+    }
+    return p;
+}
+
+__device__ __forceinline__ int64_t paged_row(const PagedMeta& m, int64_t page, int32_t g, int32_t off) {
+    return page * m.page_stride + g * m.head_stride + off * m.token_stride;
+}
+
+}  // namespace splitkv

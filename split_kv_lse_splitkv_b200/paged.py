@@ -1,0 +1,255 @@
+"""A paged key-value cache and the calls that serve tokens from it: append, page selection, decode attention.
+
+:class:`PagedKV` holds the caches, the scratch and the status word and marshals tensors into the C ABI's
+``splitkv_paged_*`` calls; every step runs in that library's kernels.
+"""
+from __future__ import annotations
+
+import threading
+from typing import Optional
+
+import torch
+
+from . import binding as B
+from .binding import EINVAL, SplitKVError
+
+_COUNTERS = 4096  # bytes at the head of the workspace that have to be zero before its first use
+
+
+def rope_table(n_positions: int, rope_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """float32 [n_positions, rope_dim]: for position p the cosines, then the sines, of p * base^(-2i/rope_dim). The
+    angles are formed in float64: at position 10^6 a float32 angle is off by 0.03."""
+    if n_positions < 1 or rope_dim < 2 or rope_dim % 2 or not base > 0:
+        raise SplitKVError(EINVAL, "rope_table")
+    freq = float(base) ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / rope_dim)
+    angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat((angle.cos(), angle.sin()), 1).to(torch.float32)
+
+
+def _need(ok, what: str) -> None:
+    if not ok:
+        raise SplitKVError(EINVAL, what)
+
+
+class PagedKV:
+    """The paged cache of one attention layer and its calls.
+
+    ``k_cache`` and ``v_cache`` are [n_pages, n_kv_heads, page_size, head_dim] tensors of equal strides (any order
+    of the outer dimensions in memory: pass a transposed view of a [n_pages, page_size, n_kv_heads, head_dim]
+    tensor as it is); without them they are allocated here from ``n_pages``, ``dtype`` and ``device``. ``k_bounds``
+    [n_pages, n_kv_heads, 2, head_dim] holds each page's smallest and largest key channel and is needed for
+    :meth:`select` only (``bounds=True`` allocates it).
+
+    Every call takes a page table (int32 [n_seqs, up to max_pages]: row b lists the pages of sequence b) and is
+    enqueued on the current stream (``stream=``: on that one); none synchronizes. Lengths, tables and token lists
+    are read on the device, so a call captured into a CUDA graph follows their values at each replay. The object's
+    scratch is shared by its decode calls: on a change of stream the new one waits for the old one, and a captured
+    call has scratch of its own. Errors that only the device sees collect in :attr:`status`.
+    """
+
+    def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, max_seqs, max_pages, n_pages=None, dtype=None,
+                 k_cache=None, v_cache=None, k_bounds=None, bounds=False, scale=None, device="cuda"):
+        _need((k_cache is None) == (v_cache is None), "PagedKV: k_cache and v_cache come together")
+        if k_cache is None:
+            _need(n_pages is not None and n_pages > 0, "PagedKV: n_pages or the caches")
+            dtype = torch.bfloat16 if dtype is None else dtype
+            shape = (int(n_pages), int(n_kv_heads), int(page_size), int(head_dim))
+            k_cache = torch.empty(shape, dtype=dtype, device=device)
+            v_cache = torch.empty(shape, dtype=dtype, device=device)
+        shape = (k_cache.shape[0], int(n_kv_heads), int(page_size), int(head_dim))
+        _need(n_pages is None or n_pages == shape[0], "PagedKV: n_pages and the caches differ")
+        _need(dtype is None or dtype == k_cache.dtype, "PagedKV: dtype and the caches differ")
+        _need(tuple(k_cache.shape) == shape and tuple(v_cache.shape) == shape,
+              f"PagedKV: caches of {tuple(k_cache.shape)} and {tuple(v_cache.shape)}, not {shape}")
+        _need(v_cache.dtype == k_cache.dtype and v_cache.device == k_cache.device and
+              v_cache.stride() == k_cache.stride() and k_cache.stride(3) == 1,
+              "PagedKV: the caches need the same type, device and strides, and dense channels")
+        if k_bounds is None and bounds:
+            k_bounds = torch.empty(shape[0], shape[1], 2, shape[3], dtype=k_cache.dtype, device=k_cache.device)
+        if k_bounds is not None:
+            _need(tuple(k_bounds.shape) == (shape[0], shape[1], 2, shape[3]) and k_bounds.is_contiguous() and
+                  k_bounds.dtype == k_cache.dtype and k_bounds.device == k_cache.device,
+                  "PagedKV: k_bounds must be a dense [n_pages, n_kv_heads, 2, head_dim] tensor of the caches' type")
+        self.k_cache, self.v_cache, self.k_bounds = k_cache, v_cache, k_bounds
+        self.dtype, self.device = k_cache.dtype, k_cache.device
+        self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), shape[1], shape[3]
+        self.page_size, self.max_seqs, self.max_pages = shape[2], int(max_seqs), int(max_pages)
+        self._scale = scale
+        self._q_shape = (self.n_q_heads, self.head_dim)
+        self._kv_shape = (self.n_kv_heads, self.head_dim)
+        self._layouts = {}  # (table width, table stride) -> splitkv_paged
+        size = B.splitkv_paged_workspace_size(self._layout(self.max_pages, self.max_pages), self.max_seqs)
+        if size == 0:  # let the library say what is wrong with the description
+            B.splitkv_paged_decode(self._layout(self.max_pages, self.max_pages), self.max_seqs, None, 0, None, None, None,
+                                   None, None, 0, None, None, None, None, stream=0)
+        self._ws_bytes = size
+        self._ws = self._stream = None
+        self._lock = threading.Lock()
+        self._index = self.device.index if self.device.type == "cuda" else None
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        if self.device.type == "cuda":
+            self._ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
+            self._stream = torch.cuda.current_stream(self.device)
+
+    # -- marshalling
+    def _layout(self, width: int, stride: int) -> B.Paged:
+        got = self._layouts.get((width, stride))
+        if got is None:
+            st = self.k_cache.stride()
+            got = B.make_paged(self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.k_cache.shape[0],
+                               width, st[:3], stride, self._scale, self.dtype)
+            if len(self._layouts) < 64:
+                self._layouts[(width, stride)] = got
+        return got
+
+    def _on(self, fn, stream, *args, **kw):
+        """fn(*args, **kw) with the cache's device current, on `stream` where one is given."""
+        if self._index is None:
+            raise SplitKVError(EINVAL, f"PagedKV: the cache is on {self.device}, not on a CUDA device")
+        if stream is None:
+            with torch.cuda.device(self._index):
+                return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        _need(stream.device == self.device, "PagedKV: a stream of another device than the cache's")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    def _away(self) -> bool:
+        return self._index is None or torch._C._cuda_getDevice() != self._index
+
+    def _raw(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self._index)
+
+    def _table(self, page_table, what):
+        _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.device == self.device and
+              (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
+              f"{what}: page_table must be an int32 [n_seqs, pages] tensor on the cache's device, its rows dense")
+        n, width = page_table.shape
+        _need(n <= self.max_seqs and 1 <= width <= self.max_pages,
+              f"{what}: a page table of {n} x {width}, made for up to {self.max_seqs} x {self.max_pages}")
+        stride = page_table.stride(0) if n > 1 else width
+        _need(stride >= width, f"{what}: page_table's rows overlap")
+        return n, self._layout(width, stride)
+
+    def _list(self, t, n, what, name):
+        _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.device == self.device and
+              (n <= 1 or t.stride(0) == 1), f"{what}: {name} must be a dense int32 [{n}] tensor on the cache's device")
+
+    def _rows(self, t, n, shape, what, name) -> int:
+        """Stride between the tokens of a [n, heads, head_dim] tensor whose heads are dense."""
+        st = t.stride()
+        _need(t.dtype == self.dtype and t.dim() == 3 and t.shape[0] == n and t.shape[1:] == shape and
+              t.device == self.device and st[2] == 1 and (shape[0] == 1 or st[1] == shape[1]),
+              f"{what}: {name} must be a {self.dtype} [{n}, {shape[0]}, {shape[1]}] tensor on the cache's device, each "
+              "token's heads dense")
+        return st[0] if n > 1 else shape[0] * shape[1]
+
+    def _out(self, t, shape, dtype, what, name):
+        _need(tuple(t.shape) == shape and t.dtype == dtype and t.device == self.device and t.is_contiguous(),
+              f"{what}: {name} must be a dense {dtype} tensor of {shape} on the cache's device")
+
+    # -- the calls
+    def append(self, k, v, page_table, token_seq, token_pos, q=None, rope: Optional[torch.Tensor] = None,
+               interleaved: bool = False, q_out=None, stream=None):
+        """Writes the keys and values of new tokens ([n_tokens, n_kv_heads, head_dim]) to their sequences' pages:
+        token i goes to position ``token_pos[i]`` of sequence ``token_seq[i]``, a row of ``page_table`` (< 0:
+        padding). The tokens are strictly ascending by (sequence, position). With ``rope`` (:func:`rope_table`) the
+        keys are rotated on the way, and ``q`` [n_tokens, n_q_heads, head_dim] into the tensor returned. The
+        bounds of the pages written follow, where the object has bounds."""
+        what = "PagedKV.append"
+        n = k.shape[0] if k.dim() else 0
+        n_seqs, layout = self._table(page_table, what)
+        ks = self._rows(k, n, self._kv_shape, what, "k")
+        vs = self._rows(v, n, self._kv_shape, what, "v")
+        self._list(token_seq, n, what, "token_seq")
+        self._list(token_pos, n, what, "token_pos")
+        qs = 0 if q is None else self._rows(q, n, self._q_shape, what, "q")
+        rope_len = rope_dim = 0
+        if rope is not None:
+            _need(rope.dtype == torch.float32 and rope.dim() == 2 and rope.device == self.device and
+                  rope.is_contiguous(), f"{what}: rope must be a dense float32 [positions, rope_dim] tensor")
+            rope_len, rope_dim = rope.shape
+        _need(q is not None or q_out is None, f"{what}: q_out without q")
+        if q_out is not None:
+            self._out(q_out, (n, *self._q_shape), self.dtype, what, "q_out")
+        if stream is not None or self._away():
+            return self._on(self.append, stream, k, v, page_table, token_seq, token_pos, q, rope, interleaved, q_out)
+        if q is not None and q_out is None:
+            q_out = torch.empty((n, *self._q_shape), dtype=self.dtype, device=self.device)
+        B.splitkv_paged_append(layout, n_seqs, n, q, qs, k, ks, v, vs, rope, rope_dim, rope_len, interleaved,
+                               page_table, token_seq, token_pos, q_out, self.k_cache, self.v_cache, self.k_bounds,
+                               self.status, self._raw())
+        return q_out
+
+    def select(self, q, page_table, seq_lens, n_select, keep_first=1, keep_last=1, pages=None, stream=None):
+        """int32 [n_seqs, n_kv_heads, n_select]: the pages (indices into the sequence's row of ``page_table``) that
+        the new token of each sequence reads at each kv head, ascending, then -1. The first ``keep_first`` and last
+        ``keep_last`` pages are always among them, the others are those with the largest bound on their scores."""
+        what = "PagedKV.select"
+        _need(self.k_bounds is not None, f"{what}: the cache has no bounds (PagedKV(..., bounds=True))")
+        n, layout = self._table(page_table, what)
+        qs = self._rows(q, n, self._q_shape, what, "q")
+        self._list(seq_lens, n, what, "seq_lens")
+        n_select = int(n_select)
+        _need(n_select >= 1 and keep_first >= 0 and keep_last >= 0, f"{what}: n_select, keep_first, keep_last")
+        if pages is not None:
+            self._out(pages, (n, self.n_kv_heads, n_select), torch.int32, what, "pages")
+        if stream is not None or self._away():
+            return self._on(self.select, stream, q, page_table, seq_lens, n_select, keep_first, keep_last, pages)
+        if pages is None:
+            pages = torch.empty((n, self.n_kv_heads, n_select), dtype=torch.int32, device=self.device)
+        B.splitkv_paged_select(layout, n, q, qs, self.k_bounds, page_table, seq_lens, n_select, keep_first, keep_last,
+                               pages, self.status, self._raw())
+        return pages
+
+    def decode(self, q, page_table, seq_lens, pages=None, o=None, lse=None, stream=None):
+        """(o, lse): attention of one new token of each sequence (q [n_seqs, n_q_heads, head_dim]) over the sequence's
+        cached keys, the first ``seq_lens[b]`` positions of row b, or over the pages of them that ``pages``
+        (:meth:`select`) lists. A sequence without keys gets o = 0, lse = -inf. To attend several new tokens
+        of a sequence, list its row once for each, with the length that the token sees."""
+        what = "PagedKV.decode"
+        n, layout = self._table(page_table, what)
+        qs = self._rows(q, n, self._q_shape, what, "q")
+        self._list(seq_lens, n, what, "seq_lens")
+        n_select = 0
+        if pages is not None:
+            n_select = pages.shape[2] if pages.dim() == 3 else 0
+            _need(n_select >= 1, f"{what}: pages must be [n_seqs, n_kv_heads, n_select]")
+            self._out(pages, (n, self.n_kv_heads, n_select), torch.int32, what, "pages")
+        if o is not None:
+            self._out(o, (n, *self._q_shape), self.dtype, what, "o")
+        if lse is not None:
+            self._out(lse, (n, self.n_q_heads), torch.float32, what, "lse")
+        if stream is not None or self._away():
+            return self._on(self.decode, stream, q, page_table, seq_lens, pages, o, lse)
+        if o is None:
+            o = torch.empty((n, *self._q_shape), dtype=self.dtype, device=self.device)
+        if lse is None:
+            lse = torch.empty((n, self.n_q_heads), dtype=torch.float32, device=self.device)
+        raw = self._raw()
+        if torch._C._cuda_isCurrentStreamCapturing():
+            # The graph may be replayed beside other work of this object: scratch of its own, its counters zeroed
+            # by the graph.
+            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+            ws[:_COUNTERS].zero_()
+            B.splitkv_paged_decode(layout, n, q, qs, self.k_cache, self.v_cache, page_table, seq_lens, pages, n_select,
+                                   o, lse, self.status, ws, raw)
+            return o, lse
+        with self._lock:
+            if raw != self._stream.cuda_stream:  # the scratch is used in turn
+                now = torch.cuda.current_stream(self.device)
+                now.wait_stream(self._stream)
+                self._stream = now
+            B.splitkv_paged_decode(layout, n, q, qs, self.k_cache, self.v_cache, page_table, seq_lens, pages, n_select,
+                                   o, lse, self.status, self._ws, raw)
+        return o, lse
+
+    # -- host-side reads (synchronizing; for tests and reports)
+    def status_value(self) -> int:
+        return int(self.status.item())
+
+    def check_status(self):
+        st = self.status_value()
+        if st:
+            raise RuntimeError(f"device status word 0x{st:x}")

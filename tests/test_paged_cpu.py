@@ -1,0 +1,281 @@
+"""The paged-cache operators without a GPU: the oracle against explicit formulas, and every refusal before a launch."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as OP
+
+B = pytest.importorskip("split_kv_lse_splitkv_b200.binding", reason="libsplitkv.so not built")
+from split_kv_lse_splitkv_b200.paged import PagedKV, rope_table  # noqa: E402
+
+
+# ------------------------------------------------------------------ the oracle
+def test_oracle_decode_is_softmax_attention(rng):
+    q, k, v = rng.standard_normal((2, 4, 8)), rng.standard_normal((5, 2, 4, 8)), rng.standard_normal((5, 2, 4, 8))
+    table = np.array([[3, 1, 0], [4, 2, 2]])
+    o, lse, _, _ = OP.decode(q, k, v, table, [9, 0], 0.3)
+    rows_k = np.concatenate([k[3], k[1], k[0]], 1)[:, :9]
+    rows_v = np.concatenate([v[3], v[1], v[0]], 1)[:, :9]
+    for h in range(4):
+        s = 0.3 * rows_k[h // 2] @ q[0, h]
+        p = np.exp(s) / np.exp(s).sum()
+        assert np.allclose(o[0, h], p @ rows_v[h // 2], rtol=1e-12) and np.isclose(lse[0, h], np.log(np.exp(s).sum()))
+    assert (o[1] == 0).all() and (lse[1] == -np.inf).all()
+    # All pages listed: the same; the parts over two lists join to the whole.
+    both = OP.decode(q[:1], k, v, table[:1], [9], 0.3, pages=np.array([[[0, 1, 2]] * 2]))
+    assert np.allclose(both[0], o[:1]) and np.allclose(both[1], lse[:1])
+    parts = [OP.decode(q[:1], k, v, table[:1], [9], 0.3, pages=np.array([[x] * 2])) for x in ([0, 2], [1])]
+    L = np.logaddexp(parts[0][1], parts[1][1])
+    joined = sum(np.exp(x[1] - L)[..., None] * x[0] for x in parts)
+    assert np.allclose(L, lse[:1]) and np.allclose(joined, o[:1])
+
+
+def test_oracle_rope_is_a_rotation(rng):
+    # The product of two rotated rows depends on the distance of their positions only, in either pairing.
+    table = rope_table(40, 6, base=100.0, device="cpu").double().numpy()
+    q, k = rng.standard_normal((1, 10)), rng.standard_normal((1, 10))
+    for pairs in (False, True):
+        dots = [(OP.rope(q, table[i + 7, :3], table[i + 7, 3:], pairs) @ OP.rope(k, table[i, :3], table[i, 3:], pairs).T)
+                for i in (0, 11, 32)]
+        assert np.allclose(dots, dots[0], atol=1e-6)  # the table is float32
+        assert np.allclose(OP.rope(q, table[0, :3], table[0, 3:], pairs), q)
+
+
+def test_oracle_scores_bound_every_key(rng):
+    q, k = rng.standard_normal((6, 5)), rng.standard_normal((7, 2, 4, 5))
+    bounds = np.stack([k.min(2), k.max(2)], 2)
+    s = OP.scores(q, bounds, np.arange(7), 1, 7)
+    real = np.einsum("hd,ptd->pt", q[3:], k[:, 1])
+    assert (real.max(1) <= s + 1e-12).all()
+    # The linear form that the kernels use.
+    up, down = np.maximum(q[3:], 0).sum(0), np.minimum(q[3:], 0).sum(0)
+    assert np.allclose(s, bounds[:, 1, 1] @ up + bounds[:, 1, 0] @ down)
+
+
+def test_oracle_select_ties_and_kept_pages():
+    q = np.ones((1, 1, 2))
+    bounds = np.zeros((6, 1, 2, 2))
+    bounds[:, 0, 1] = np.array([0, 5, 5, 1, 5, 0])[:, None]
+    table = np.arange(6)[None]
+    assert OP.select(q, bounds, table, [12], 2, 2, 0, 0)[0, 0].tolist() == [1, 2]
+    assert OP.select(q, bounds, table, [11], 2, 4, 1, 1)[0, 0].tolist() == [0, 1, 2, 5]
+    assert OP.select(q, bounds, table, [11], 2, 2, 2, 2)[0, 0].tolist() == [0, 1]
+    assert OP.select(q, bounds, table, [3], 2, 4, 1, 1)[0, 0].tolist() == [0, 1, -1, -1]
+    assert OP.select(q, bounds, table, [0], 2, 2, 1, 1)[0, 0].tolist() == [-1, -1]
+
+
+def test_rope_table():
+    t = rope_table(5, 8, base=1000.0, device="cpu")
+    assert t.shape == (5, 8) and t.dtype == torch.float32
+    ang = 3 * 1000.0 ** (-np.arange(4) / 4)
+    assert np.allclose(t[3].numpy(), np.concatenate([np.cos(ang), np.sin(ang)]), atol=1e-7)
+    # A far position: the angle itself is right to float64, not to float32.
+    far = rope_table(1 << 20, 2, device="cpu")[-1].numpy()
+    assert abs(far[0] - np.cos(float((1 << 20) - 1))) < 1e-7
+    for bad in ((0, 8), (4, 7), (4, 0)):
+        with pytest.raises(B.SplitKVError):
+            rope_table(*bad, device="cpu")
+
+
+# ------------------------------------------------------------------ the C ABI's refusals
+def desc(**kw):
+    a = dict(n_q_heads=8, n_kv_heads=2, head_dim=64, page_size=16, n_pages=10, max_pages=4,
+             strides=(2 * 16 * 64, 16 * 64, 64), dtype=torch.bfloat16)
+    a.update(kw)
+    return B.make_paged(**a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_q_heads=7), B.EINVAL),
+    (dict(n_kv_heads=0), B.EINVAL),
+    (dict(head_dim=60), B.EUNSUPPORTED),                                   # not a multiple of 16 bytes
+    (dict(head_dim=136, strides=(2 * 16 * 136, 16 * 136, 136)), B.EUNSUPPORTED),
+    (dict(page_size=12), B.EUNSUPPORTED),                                  # not a power of two
+    (dict(page_size=2048), B.EUNSUPPORTED),
+    (dict(page_size=0), B.EINVAL),
+    (dict(n_pages=0), B.EINVAL),
+    (dict(max_pages=0), B.EINVAL),
+    (dict(max_pages=1 << 28), B.EUNSUPPORTED),                             # a sequence of 2^32 positions
+    (dict(table_stride=3), B.EINVAL),
+    (dict(scale=0.0), B.EINVAL),
+    (dict(scale=float("nan")), B.EINVAL),
+    (dict(scale=float("inf")), B.EINVAL),
+    (dict(strides=(2 * 16 * 64, 16 * 64, 60)), B.EINVAL),                  # rows overlap
+    (dict(strides=(2 * 16 * 64, 15 * 64, 64)), B.EINVAL),                  # heads overlap
+    (dict(strides=(16 * 64, 16 * 64, 64)), B.EINVAL),                      # pages overlap
+    (dict(strides=(2 * 16 * 64 + 4, 16 * 64, 64)), B.EINVAL),              # not a multiple of 16 bytes
+    (dict(strides=(0, 16 * 64, 64)), B.EINVAL),
+])
+def test_bad_descriptions_are_refused(kw, code):
+    fake = torch.empty(64, dtype=torch.int32)
+    p = desc(**kw)
+    assert B.splitkv_paged_workspace_size(p, 4) == 0
+    with pytest.raises(B.SplitKVError) as e:
+        B.splitkv_paged_decode(p, 4, fake, 512, fake, fake, fake, fake, None, 0, fake, fake, fake, fake, stream=0)
+    assert e.value.code == code
+
+
+def test_layouts_that_are_accepted():
+    for kw in (dict(), dict(strides=(2 * 16 * 64, 64, 128)),               # [pages, positions, heads, d]
+               dict(strides=(16 * 64, 10 * 16 * 64, 64)),                  # [heads, pages, positions, d]
+               dict(strides=(2 * 16 * 80, 16 * 80, 80)),                   # rows with a gap
+               dict(page_size=1, strides=(128, 64, 8)),                    # one position a page: its stride says nothing
+               dict(head_dim=8, strides=(2 * 16 * 8, 16 * 8, 8)),
+               dict(dtype=torch.float32, head_dim=12, strides=(2 * 16 * 12, 16 * 12, 12))):
+        assert B.splitkv_paged_workspace_size(desc(**kw), 4) > 0
+    assert B.splitkv_paged_workspace_size(desc(), 0) > 0
+    assert B.splitkv_paged_workspace_size(desc(), -1) == 0
+    assert B.splitkv_paged_workspace_size(desc(), B.PAGED_MAX_SEQS + 1) == 0
+
+
+def test_decode_refusals():
+    f = torch.empty(1 << 16, dtype=torch.int32)  # host memory, never dereferenced
+    ws = torch.empty(B.splitkv_paged_workspace_size(desc(), 4), dtype=torch.uint8)
+    good = dict(q=f, q_stride=512, k_cache=f, v_cache=f, page_table=f, seq_len=f, pages=None, n_select=0, o=f, lse=f,
+                status=f, workspace=ws)
+    for kw, code in ((dict(q=None), B.EINVAL), (dict(k_cache=None), B.EINVAL), (dict(v_cache=None), B.EINVAL),
+                     (dict(page_table=None), B.EINVAL), (dict(seq_len=None), B.EINVAL), (dict(o=None), B.EINVAL),
+                     (dict(lse=None), B.EINVAL), (dict(status=None), B.EINVAL), (dict(q=f[1:]), B.EINVAL),
+                     (dict(k_cache=f[1:]), B.EINVAL), (dict(v_cache=f[2:]), B.EINVAL), (dict(o=f[3:]), B.EINVAL),
+                     (dict(q_stride=504), B.EINVAL), (dict(q_stride=516), B.EINVAL), (dict(q_stride=-512), B.EINVAL),
+                     (dict(pages=f, n_select=0), B.EINVAL), (dict(workspace=None), B.ENOSPACE),
+                     (dict(workspace=ws[:64]), B.ENOSPACE), (dict(workspace=ws[8:]), B.ENOSPACE)):
+        with pytest.raises(B.SplitKVError) as e:
+            B.splitkv_paged_decode(desc(), 4, **{**good, **kw}, stream=0)
+        assert e.value.code == code, kw
+    with pytest.raises(B.SplitKVError) as e:
+        B.splitkv_paged_decode(desc(), B.PAGED_MAX_SEQS + 1, **good, stream=0)
+    assert e.value.code == B.EUNSUPPORTED
+    # No sequence: nothing to do, no tensor is looked at.
+    B.splitkv_paged_decode(desc(), 0, **{k: None for k in good} | dict(q_stride=0, n_select=0, status=f), stream=0)
+
+
+def test_append_refusals():
+    f = torch.empty(1 << 16, dtype=torch.int32)
+    far = torch.empty(1 << 16, dtype=torch.int32)
+    good = dict(n_seqs=4, n_tokens=5, q=f, q_stride=512, k=f, k_stride=128, v=f, v_stride=128, rope=f, rope_dim=64,
+                rope_len=100, interleaved=0, page_table=f, token_seq=f, token_pos=f, q_out=far, k_cache=f, v_cache=f,
+                k_bounds=f, status=f)
+    for kw, code in ((dict(k=None), B.EINVAL), (dict(v=None), B.EINVAL), (dict(q_out=None), B.EINVAL),
+                     (dict(page_table=None), B.EINVAL), (dict(token_seq=None), B.EINVAL),
+                     (dict(token_pos=None), B.EINVAL), (dict(k_cache=None), B.EINVAL), (dict(v_cache=None), B.EINVAL),
+                     (dict(status=None), B.EINVAL), (dict(n_tokens=-1), B.EINVAL), (dict(k_stride=64), B.EINVAL),
+                     (dict(v_stride=132), B.EINVAL), (dict(q_stride=256), B.EINVAL), (dict(k=f[1:]), B.EINVAL),
+                     (dict(k_bounds=f[1:]), B.EINVAL), (dict(rope=f[1:]), B.EINVAL), (dict(rope_dim=0), B.EINVAL),
+                     (dict(rope_dim=63), B.EINVAL), (dict(rope_dim=66), B.EINVAL), (dict(rope_len=0), B.EINVAL),
+                     (dict(rope=None), B.EINVAL),                            # rope_dim without a table
+                     (dict(q_out=f), B.EINVAL), (dict(q_out=f[128:]), B.EINVAL),  # over q itself
+                     (dict(n_seqs=-1), B.EINVAL), (dict(n_tokens=1 << 31), B.EUNSUPPORTED)):
+        with pytest.raises(B.SplitKVError) as e:
+            B.splitkv_paged_append(desc(), **{**good, **kw}, stream=0)
+        assert e.value.code == code, kw
+    B.splitkv_paged_append(desc(), **{**good, **dict(n_tokens=0, k=None, v=None, q=None, q_out=None)}, stream=0)
+
+
+def test_select_refusals():
+    f = torch.empty(1 << 16, dtype=torch.int32)
+    good = dict(n_seqs=4, q=f, q_stride=512, k_bounds=f, page_table=f, seq_len=f, n_select=3, keep_first=1, keep_last=1,
+                pages=f, status=f)
+    for kw, code in ((dict(q=None), B.EINVAL), (dict(k_bounds=None), B.EINVAL), (dict(page_table=None), B.EINVAL),
+                     (dict(seq_len=None), B.EINVAL), (dict(pages=None), B.EINVAL), (dict(status=None), B.EINVAL),
+                     (dict(n_select=0), B.EINVAL), (dict(keep_first=-1), B.EINVAL), (dict(keep_last=-1), B.EINVAL),
+                     (dict(k_bounds=f[2:]), B.EINVAL), (dict(n_select=B.PAGED_MAX_SELECT_PAGES + 1), B.EUNSUPPORTED)):
+        with pytest.raises(B.SplitKVError) as e:
+            B.splitkv_paged_select(desc(), **{**good, **kw}, stream=0)
+        assert e.value.code == code, kw
+    with pytest.raises(B.SplitKVError) as e:
+        B.splitkv_paged_select(desc(max_pages=B.PAGED_MAX_SELECT_PAGES + 1), **good, stream=0)
+    assert e.value.code == B.EUNSUPPORTED
+    B.splitkv_paged_select(desc(), **{**good, "n_seqs": 0}, stream=0)
+
+
+# ------------------------------------------------------------------ the class's refusals
+def make(**kw):
+    a = dict(n_q_heads=8, n_kv_heads=2, head_dim=64, page_size=16, max_seqs=4, max_pages=6, n_pages=10, bounds=True,
+             device="cpu")
+    a.update(kw)
+    return PagedKV(**a)
+
+
+def test_class_construction_refusals():
+    kv = make()
+    assert kv.k_cache.shape == (10, 2, 16, 64) and kv.k_bounds.shape == (10, 2, 2, 64) and kv.dtype == torch.bfloat16
+    c = torch.zeros(10, 2, 16, 64, dtype=torch.bfloat16)
+    make(n_pages=None, k_cache=c, v_cache=c.clone(), bounds=False)
+    t = torch.zeros(10, 16, 2, 64).transpose(1, 2)
+    assert make(n_pages=None, k_cache=t, v_cache=torch.zeros(10, 16, 2, 64).transpose(1, 2)).dtype == torch.float32
+    for kw in (dict(n_pages=None), dict(n_pages=0), dict(k_cache=c), dict(k_cache=c, v_cache=c[:, :, :8]),
+               dict(k_cache=c, v_cache=c.float()), dict(k_cache=c, v_cache=c, n_pages=9),
+               dict(k_cache=c, v_cache=c, dtype=torch.float32),
+               dict(k_cache=c.expand(10, 2, 16, 64), v_cache=torch.zeros(10, 16, 2, 64, dtype=c.dtype).transpose(1, 2)),
+               dict(k_cache=c[..., ::2].repeat(1, 1, 1, 2)[..., :64], v_cache=c, k_bounds=c),
+               dict(k_cache=c[:1].expand(10, 2, 16, 64), v_cache=c[:1].expand(10, 2, 16, 64)),  # pages overlap
+               dict(dtype=torch.float16), dict(n_q_heads=9), dict(page_size=24), dict(head_dim=130), dict(scale=-1.0),
+               dict(max_pages=0), dict(max_seqs=B.PAGED_MAX_SEQS + 1)):
+        with pytest.raises(B.SplitKVError):
+            make(**kw)
+
+
+def bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def calls(kv):
+    return {
+        "decode": (kv.decode, dict(q=bf(3, 8, 64), page_table=i32(3, 6), seq_lens=i32(3))),
+        "select": (kv.select, dict(q=bf(3, 8, 64), page_table=i32(3, 6), seq_lens=i32(3), n_select=2)),
+        "append": (kv.append, dict(k=bf(5, 2, 64), v=bf(5, 2, 64), page_table=i32(3, 6), token_seq=i32(5), token_pos=i32(5),
+                                   q=bf(5, 8, 64), rope=torch.zeros(96, 64))),
+    }
+
+
+@pytest.mark.parametrize("name", ["decode", "select", "append"])
+def test_well_formed_calls_reach_the_device_check(name):
+    fn, kw = calls(make())[name]
+    with pytest.raises(B.SplitKVError, match="not on a CUDA device"):
+        fn(**kw)
+
+
+def _q_strided():
+    return bf(3, 16, 64)[:, ::2]
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("decode", dict(q=bf(3, 8, 32))), ("decode", dict(q=bf(2, 8, 64))), ("decode", dict(q=bf(3, 8, 64).float())),
+    ("decode", dict(q=bf(3, 64, 8).transpose(1, 2))), ("decode", dict(q=_q_strided())), ("decode", dict(q=bf(3, 512))),
+    ("decode", dict(page_table=i32(3, 7))), ("decode", dict(page_table=i32(5, 6))), ("decode", dict(page_table=i32(18))),
+    ("decode", dict(page_table=i32(3, 6).long())), ("decode", dict(page_table=i32(6, 3).t())),
+    ("decode", dict(page_table=i32(1, 6).expand(3, 6))), ("decode", dict(page_table=i32(3, 0))),
+    ("decode", dict(seq_lens=i32(2))), ("decode", dict(seq_lens=i32(3).long())), ("decode", dict(seq_lens=i32(6)[::2])),
+    ("decode", dict(pages=i32(3, 2, 0))), ("decode", dict(pages=i32(3, 8, 2))), ("decode", dict(pages=i32(3, 2, 4)[..., :2])),
+    ("decode", dict(pages=i32(3, 2, 2).long())), ("decode", dict(o=bf(3, 8, 32))), ("decode", dict(o=bf(8, 3, 64).transpose(0, 1))),
+    ("decode", dict(lse=bf(3, 8))), ("decode", dict(lse=torch.zeros(8, 3).t())),
+    ("select", dict(n_select=0)), ("select", dict(keep_first=-1)), ("select", dict(keep_last=-2)),
+    ("select", dict(pages=i32(3, 2, 3))), ("select", dict(seq_lens=i32(4))), ("select", dict(q=bf(3, 4, 64))),
+    ("append", dict(k=bf(5, 8, 64))), ("append", dict(v=bf(4, 2, 64))), ("append", dict(token_seq=i32(4))),
+    ("append", dict(token_pos=i32(5).long())), ("append", dict(rope=torch.zeros(96, 64).bfloat16())),
+    ("append", dict(rope=torch.zeros(64, 96).t())), ("append", dict(q=None, q_out=bf(5, 8, 64))),
+    ("append", dict(q_out=bf(5, 8, 32))), ("append", dict(q=bf(4, 8, 64))), ("append", dict(k=torch.zeros(()).bfloat16())),
+])
+def test_class_call_refusals(name, bad):
+    fn, kw = calls(make())[name]
+    with pytest.raises(B.SplitKVError) as e:
+        fn(**{**kw, **bad})
+    assert e.value.code == B.EINVAL and "CUDA device" not in str(e.value)
+
+
+def test_select_needs_bounds():
+    kv = make(bounds=False)
+    with pytest.raises(B.SplitKVError, match="bounds"):
+        kv.select(bf(3, 8, 64), i32(3, 6), i32(3), 2)
+
+
+def test_struct_matches_the_header():
+    # The compiler's size of splitkv_paged: four int32, one int64, an int32 (padded), four int64, float, int32.
+    assert ctypes.sizeof(B.Paged) == 16 + 8 + 8 + 32 + 8
