@@ -414,7 +414,8 @@ int splitkv_paged_append(const splitkv_paged *paged, int32_t n_seqs, int64_t n_t
  * Decode attention: for each sequence b and query head h (kv head g = h / (Hq/Hkv)), over the cached keys
  * j < seq_len_d[b]:
  *   s_j = scale * q_bh . k_j,  lse_bh = log sum_j exp(s_j) (natural log),  o_bh = sum_j exp(s_j - lse_bh) v_j
- * A row without keys (length 0, or only scores of -inf) gets o = 0, lse = -inf. Cache positions at or past
+ * A row without keys (length 0, or only scores of -inf) gets o = 0, lse = -inf; where an infinite value
+ * is read, o may be NaN. Cache positions at or past
  * the length are not read. pages_d NULL: every key. Otherwise pages_d [n_seqs, Hkv, n_select] lists the page-table
  * entries (page p: positions p*page_size ..) to read for (b, g): strictly ascending, within the sequence's
  * pages, the unused tail filled with -1 (anything else: SPLITKV_DEV_BAD_PAGE).
