@@ -27,6 +27,8 @@ using sm100::ex2_approx;
 constexpr int kTile = 16;          // keys of a unit
 constexpr int kMaxParts = 512;     // most blocks that share the work: counters and partial slots of the workspace
 constexpr size_t kCounterBytes = 4096;
+constexpr int kSegmentCost = 4;    // units that the beginning of a segment counts
+constexpr int kAlone = 6;          // tiles a warp may have for a block to take a whole segment, without a join of blocks
 constexpr float kLazy = 8.f;       // log2 units a score may exceed the reference before the reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxDP = 128, kMaxRows = 16;
@@ -346,23 +348,27 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
 }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 
-// Everything a block needs to know about the line of units.
-struct Line {
-    const int32_t* prefix;  // shared: tiles of the sequences before b (of one kv head)
-    int32_t n_seqs, per_seq;  // per_seq = kv heads x groups of query rows: segments of a sequence
-    int64_t total;
-    int32_t parts;
+// a / b for values that nearly always fit 32 bits.
+__device__ __noinline__ int64_t div_wide(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : div_wide(a, b);
+}
 
-    __device__ __forceinline__ int64_t lo(int64_t c) const { return total * c / parts; }
-    __device__ __forceinline__ int32_t part_of(int64_t u) const {  // the part that holds unit u
-        return (int32_t)(((u + 1) * parts - 1) / total);
-    }
+// The line of units. A segment (sequence, kv head, group of query rows) takes kSegmentCost units before its tiles': what
+// it costs to begin one (table, queries, first keys: one after the other) next to the streaming of a tile.
+struct Line {
+    const int32_t* prefix;    // shared: units of the sequences before b, for one segment of each
+    int32_t n_seqs, per_seq;  // per_seq = kv heads x groups of query rows: segments of a sequence
+    int64_t total, per_part;
+
+    __device__ __forceinline__ int32_t part_of(int64_t u) const { return (int32_t)div_units(u, per_part); }
 };
 
-// One segment as seen from a unit of it.
 struct Segment {
-    int32_t b, sub, tile, tiles;  // sequence, kv head and row group, tile of the unit, tiles in all
-    int64_t start;                // first unit
+    int32_t b, sub, tiles;  // sequence, kv head and row group, tiles
+    int64_t start;          // first unit; its tiles begin at start + kSegmentCost
+    __device__ __forceinline__ int64_t tile0() const { return start + kSegmentCost; }
+    __device__ __forceinline__ int64_t end() const { return start + kSegmentCost + tiles; }
 };
 
 __device__ __forceinline__ Segment segment_at(const Line& L, int64_t u) {
@@ -371,13 +377,13 @@ __device__ __forceinline__ Segment segment_at(const Line& L, int64_t u) {
         const int32_t mid = (lo + hi) >> 1;
         if ((int64_t)L.prefix[mid] * L.per_seq <= u) lo = mid; else hi = mid;
     }
+    const int32_t width = L.prefix[lo + 1] - L.prefix[lo];
+    const int64_t base = (int64_t)L.prefix[lo] * L.per_seq;
     Segment s;
     s.b = lo;
-    s.tiles = L.prefix[lo + 1] - L.prefix[lo];
-    const int64_t rem = u - (int64_t)L.prefix[lo] * L.per_seq;
-    s.sub = (int32_t)(rem / s.tiles);
-    s.tile = (int32_t)(rem - (int64_t)s.sub * s.tiles);
-    s.start = u - s.tile;
+    s.tiles = width - kSegmentCost;
+    s.sub = (int32_t)div_units(u - base, width);
+    s.start = base + (int64_t)s.sub * width;
     return s;
 }
 
@@ -388,6 +394,21 @@ struct Partial {
     float m[R], l[R];
 };
 
+// A segment whose parts a block joins.
+struct Group {
+    int32_t first, n;  // its parts in the block's list of them
+    int32_t rows;
+    int32_t out;       // -1: the results; 0, 1: the block's part of the segment that it entered, that it leaves
+    int64_t h;         // first row of the results
+};
+
+// A segment that several blocks hold.
+struct Side {
+    int32_t first, n;  // the blocks, 0: none
+    int32_t rows, last;
+    int64_t h;
+};
+
 template <typename T, int DP, int NT, int W>
 __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
                                                           const T* __restrict__ kc, const T* __restrict__ vc,
@@ -396,93 +417,131 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
                                                           const int32_t* __restrict__ pages, int32_t n_select,
                                                           T* __restrict__ o, float* __restrict__ lse, int32_t* status,
                                                           uint32_t* counters, char* slots) {
-    constexpr int R = 8 * NT;
+    static_assert(2 * W <= 32, "one lane per partial of the block");
+    constexpr int R = 8 * NT, kCols = DP / 4, kThreads = W * 32;
     using P = Partial<DP, R>;
     extern __shared__ __align__(16) char smem[];
-    P* part = reinterpret_cast<P*>(smem);  // [W][2]
-    __shared__ int64_t seg_of[W][2];       // first unit of the segment a warp's partial belongs to, -1: none
-    __shared__ int32_t shared_flag[3];     // status seen, and whether this block joins its left, its right segment
+    P* part = reinterpret_cast<P*>(smem);  // [W][2]: a warp's part of the segment it entered, of the one it left
+    __shared__ int64_t seg_of[2 * W];      // first unit of the segment that part belongs to, -1: none
+    __shared__ int32_t list[2 * W];        // the parts there are
+    __shared__ float weight[2 * W][R];
+    __shared__ float scale_of[2 * W][R];   // 1 / sum of a finished row
+    __shared__ Group group[2 * W];
+    __shared__ Side side[2];
     int32_t* prefix = reinterpret_cast<int32_t*>(smem + sizeof(P) * W * 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row_groups = (m.group + R - 1) / R;
 
     // ---- the line of units
-    if (tid == 0) shared_flag[0] = status_bad(status);
-    for (int b = tid; b < m.n_seqs; b += W * 32) {
+    const bool skip = status_bad(status);
+    auto units_of = [&](int b) {
         const int32_t len = paged_len(m, seq_len, b, status);
         int32_t n = len;
         if (pages) n = min(n_select, (len + m.page - 1) >> m.page_shift) << m.page_shift;
-        prefix[b + 1] = (n + kTile - 1) / kTile;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int32_t carry = 0;
-        for (int b0 = 0; b0 < m.n_seqs; b0 += 32) {
-            int32_t x = b0 + lane < m.n_seqs ? prefix[b0 + lane + 1] : 0;
-            for (int s = 1; s < 32; s <<= 1) {
-                const int32_t y = __shfl_up_sync(0xffffffffu, x, s);
-                if (lane >= s) x += y;
-            }
-            if (b0 + lane < m.n_seqs) prefix[b0 + lane + 1] = carry + x;
-            carry += __shfl_sync(0xffffffffu, x, 31);
+        return n ? (n + kTile - 1) / kTile + kSegmentCost : 0;
+    };
+    if (lane < 2) seg_of[warp * 2 + lane] = -1;
+    bool empties;      // some sequence has no keys
+    int32_t widest;    // units of the longest segment
+    if (m.n_seqs <= 32) {  // each warp by itself
+        int32_t x = lane < m.n_seqs ? units_of(lane) : 0;
+        empties = __any_sync(0xffffffffu, lane < m.n_seqs && x == 0);
+        widest = __reduce_max_sync(0xffffffffu, x);
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, x, s);
+            if (lane >= s) x += y;
         }
+        prefix += warp * 36;
+        prefix[lane + 1] = x;
         if (lane == 0) prefix[0] = 0;
+        __syncwarp();
+    } else {
+        int32_t most = 0;
+        bool none = false;
+        for (int b = tid; b < m.n_seqs; b += kThreads) {
+            const int32_t x = units_of(b);
+            prefix[b + 1] = x;
+            none |= x == 0;
+            most = max(most, x);
+        }
+        empties = __syncthreads_or(none);
+        widest = __syncthreads_or(most > kAlone * W) ? INT32_MAX : 0;
+        if (warp == 0) {
+            int32_t carry = 0;
+            for (int b0 = 0; b0 < m.n_seqs; b0 += 32) {
+                int32_t x = b0 + lane < m.n_seqs ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int32_t y = __shfl_up_sync(0xffffffffu, x, s);
+                    if (lane >= s) x += y;
+                }
+                if (b0 + lane < m.n_seqs) prefix[b0 + lane + 1] = carry + x;
+                carry += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) prefix[0] = 0;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const bool skip = shared_flag[0];
     Line L{prefix, m.n_seqs, m.hkv * row_groups, 0, 0};
     L.total = (int64_t)prefix[m.n_seqs] * L.per_seq;
-    const int64_t want = (L.total + W - 1) / W;
-    L.parts = (int32_t)(want < gridDim.x ? want : gridDim.x);
+    L.per_part = max(div_units(L.total + gridDim.x - 1, gridDim.x), (int64_t)W);
 
     // ---- sequences without keys
-    if (!skip)
+    if (empties && !skip)
         for (int b = blockIdx.x; b < m.n_seqs; b += gridDim.x) {
             if (prefix[b + 1] > prefix[b]) continue;
-            for (int i = tid; i < m.hq * m.d; i += W * 32) o[(int64_t)b * m.hq * m.d + i] = from_f32<T>(0.f);
-            for (int h = tid; h < m.hq; h += W * 32) lse[(int64_t)b * m.hq + h] = -INFINITY;
+            for (int i = tid; i < m.hq * m.d; i += kThreads) o[(int64_t)b * m.hq * m.d + i] = from_f32<T>(0.f);
+            for (int h = tid; h < m.hq; h += kThreads) lse[(int64_t)b * m.hq + h] = -INFINITY;
             if (pages)
-                for (int i = tid; i < m.hkv * n_select; i += W * 32)
+                for (int i = tid; i < m.hkv * n_select; i += kThreads)
                     if (pages[(int64_t)b * m.hkv * n_select + i] != -1) raise_status(status, SPLITKV_DEV_BAD_PAGE);
         }
-    if ((int)blockIdx.x >= L.parts) return;
-
-    const int64_t c_lo = L.lo(blockIdx.x), c_hi = L.lo(blockIdx.x + 1);
-    const int64_t w_lo = c_lo + (c_hi - c_lo) * warp / W, w_hi = c_lo + (c_hi - c_lo) * (warp + 1) / W;
-    if (lane < 2) seg_of[warp][lane] = -1;
-    __syncwarp();
+    int64_t c_lo = (int64_t)blockIdx.x * L.per_part, c_hi = min(c_lo + L.per_part, L.total);
+    if (widest <= kAlone * W && (int64_t)m.n_seqs * L.per_seq <= gridDim.x) {  // a block per segment
+        const int b = blockIdx.x / L.per_seq;
+        if (b >= m.n_seqs) return;
+        const int32_t width = prefix[b + 1] - prefix[b];
+        c_lo = (int64_t)prefix[b] * L.per_seq + (int64_t)(blockIdx.x - b * L.per_seq) * width;
+        c_hi = c_lo + width;
+    }
+    if (c_lo >= c_hi) return;
+    const int64_t units = c_hi - c_lo;
+    const int64_t w_lo = c_lo + units * warp / W, w_hi = c_lo + units * (warp + 1) / W;
 
     Frag<T, DP, NT> f;
     const float to_log2 = m.scale * kLog2e;
     for (int64_t u = skip ? w_hi : w_lo; u < w_hi;) {
         const Segment sg = segment_at(L, u);
-        const int32_t t_end = (int32_t)(w_hi - sg.start < sg.tiles ? w_hi - sg.start : sg.tiles);
+        const int32_t t_begin = (int32_t)max(u - sg.tile0(), (int64_t)0);
+        u = min(w_hi, sg.end());
+        const int32_t t_end = (int32_t)max(u - sg.tile0(), (int64_t)0);
+        if (t_end <= t_begin) continue;  // of this segment's units only those of its beginning
         const int32_t g = sg.sub / row_groups, row0 = (sg.sub - g * row_groups) * R;
         const int32_t rows = min(R, m.group - row0);
         const int32_t* trow = table + sg.b * m.table_stride;
         const int32_t len = __ldg(seq_len + sg.b), count = (len + m.page - 1) >> m.page_shift;
-        const int32_t* list = pages ? pages + ((int64_t)sg.b * m.hkv + g) * n_select : nullptr;
-        const int32_t listed = list ? min(n_select, count) : 0;
+        const int32_t* chosen = pages ? pages + ((int64_t)sg.b * m.hkv + g) * n_select : nullptr;
+        const int32_t listed = chosen ? min(n_select, count) : 0;
         const int64_t head = (int64_t)g * m.head_stride;
-        f.load_q(q + sg.b * q_stride + (int64_t)(g * m.group + row0) * m.d, rows, m.d, lane);
-        if (list && sg.tile == 0 && row0 == 0)  // the unread tail of the list has to be empty
+        if (chosen && t_begin == 0 && row0 == 0)  // the unread tail of the list has to be empty
             for (int32_t i = listed + lane; i < n_select; i += 32)
-                if (__ldg(list + i) != -1) raise_status(status, SPLITKV_DEV_BAD_PAGE);
+                if (__ldg(chosen + i) != -1) raise_status(status, SPLITKV_DEV_BAD_PAGE);
 
         // Page-table entry of the lane's row of tile i, or -1 (past the end, or not listed).
         auto entry_of = [&](int32_t i) -> int32_t {
             const int32_t pos = i * kTile + (lane & 15), e = pos >> m.page_shift;
             if (i >= t_end) return -1;
-            if (!list) return pos < len ? e : -1;
+            if (!chosen) return pos < len ? e : -1;
             if (e >= listed) return -1;
-            const int32_t x = __ldg(list + e);
+            const int32_t x = __ldg(chosen + e);
             const bool first = (pos & (m.page - 1)) == 0 || (lane & 15) == 0;
             if (x < -1 || x >= count) {
                 raise_status(status, SPLITKV_DEV_BAD_PAGE);
                 return -1;
             }
             if (first && e > 0 && x >= 0) {
-                const int32_t y = __ldg(list + e - 1);
+                const int32_t y = __ldg(chosen + e - 1);
                 if (y < 0 || y >= x) raise_status(status, SPLITKV_DEV_BAD_PAGE);
             }
             return x;
@@ -497,25 +556,30 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
             return r;
         };
 
+        // Loads run ahead: K of the next tile is on its way during this one's softmax and PV, V during the next
+        // one's QK; page-table entries two tiles ahead, list entries three.
+        int32_t i = t_begin;
+        int32_t e1 = entry_of(i + 1), e2 = entry_of(i + 2), p1;
+        TileRows r;
+        {
+            const int32_t e0 = entry_of(i), p0 = page_of(e0);
+            p1 = page_of(e1);
+            f.load_q(q + sg.b * q_stride + (int64_t)(g * m.group + row0) * m.d, rows, m.d, lane);
+            r = rows_of(i, e0, p0);
+        }
+        f.load_k(kc, r, m.d, lane);
+        f.load_v(vc, r, m.d, lane);
+
         float mx[NT][2], ref[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) mx[n][y] = -INFINITY, ref[n][y] = 0.f, l[n][y] = 0.f;
 #pragma unroll
-            for (int i = 0; i < Frag<T, DP, NT>::kOut; ++i)
+            for (int x = 0; x < Frag<T, DP, NT>::kOut; ++x)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f.o[n][i][j] = 0.f;
+                for (int j = 0; j < 4; ++j) f.o[n][x][j] = 0.f;
         }
-
-        // Loads run ahead: K of the next tile is on its way during this one's softmax and PV, V during the next
-        // one's QK; page-table entries two tiles ahead, list entries three.
-        int32_t i = sg.tile;
-        int32_t e0 = entry_of(i), e1 = entry_of(i + 1), e2 = entry_of(i + 2);
-        int32_t p0 = page_of(e0), p1 = page_of(e1);
-        TileRows r = rows_of(i, e0, p0);
-        f.load_k(kc, r, m.d, lane);
-        f.load_v(vc, r, m.d, lane);
         for (; i < t_end; ++i) {
             const uint32_t valid = r.valid;
             r = rows_of(i + 1, e1, p1);
@@ -567,136 +631,187 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
             f.load_v(vc, r, m.d, lane);
         }
 
-        // The rows' sums over the lanes that hold their keys.
+        const int slot = warp * 2 + (t_begin == 0);
+        const bool whole = t_begin == 0 && t_end == sg.tiles;
+        const int64_t h0 = (int64_t)sg.b * m.hq + g * m.group + row0;
+        P& out = part[slot];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
+            for (int y = 0; y < 2; ++y) {
+                const int row = 8 * n + 2 * (lane & 3) + y;
+                // The row's sum over the lanes that hold its keys.
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[n][y] += __shfl_xor_sync(0xffffffffu, l[n][y], x);
-        const int t = lane & 3;
-        if (sg.tile == 0 && t_end == sg.tiles) {  // a whole segment
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int row = 8 * n + 2 * t + y;
-                    if (row >= rows) continue;
-                    const int64_t h = (int64_t)sg.b * m.hq + g * m.group + row0 + row;
-                    const float inv = l[n][y] == 0.f ? 0.f : 1.f / l[n][y];
-                    f.each(n, y, lane, [&](int c, float4 x) {
-                        if (c < m.d) store4(o + h * m.d + c, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-                    });
-                    if (lane < 4) lse[h] = l[n][y] == 0.f ? -INFINITY : (mx[n][y] + log2f(l[n][y])) * (1.f / kLog2e);
-                }
-        } else {
-            const int slot = seg_of[warp][0] >= 0;
-            __syncwarp();
-            P& out = part[warp * 2 + slot];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int row = 8 * n + 2 * t + y;
+                if (!whole) {
                     f.each(n, y, lane, [&](int c, float4 x) { *reinterpret_cast<float4*>(&out.o[row][c]) = x; });
                     if (lane < 4) out.m[row] = mx[n][y], out.l[row] = l[n][y];
+                } else if (row < rows) {
+                    const float inv = l[n][y] == 0.f ? 0.f : 1.f / l[n][y];
+                    f.each(n, y, lane, [&](int c, float4 x) {
+                        if (c < m.d)
+                            store4(o + (h0 + row) * m.d + c, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+                    });
+                    if (lane < 4)
+                        lse[h0 + row] = l[n][y] == 0.f ? -INFINITY : (mx[n][y] + log2f(l[n][y])) * (1.f / kLog2e);
                 }
-            if (lane == 0) seg_of[warp][slot] = sg.start;
-            __syncwarp();
+            }
+        if (!whole && lane == 0) seg_of[slot] = sg.start;
+    }
+
+    // ---- the segments that other blocks hold parts of: side 0 began in an earlier block, side 1 goes on in the next
+    if (warp < 2) {
+        const Segment sg = segment_at(L, warp ? c_hi - 1 : c_lo);
+        const bool open = warp ? sg.tile0() >= c_lo && sg.tile0() < c_hi && sg.end() > c_hi : sg.tile0() < c_lo;
+        if (lane == 0) {
+            const int32_t g = sg.sub / row_groups, row0 = (sg.sub - g * row_groups) * R;
+            Side x{0, 0, min(R, m.group - row0), 0, (int64_t)sg.b * m.hq + g * m.group + row0};
+            if (open) {
+                x.first = L.part_of(sg.tile0());
+                x.n = L.part_of(sg.end() - 1) - x.first + 1;
+            }
+            side[warp] = x;
         }
-        u = sg.start + t_end;
     }
     __syncthreads();
 
-    // ---- join the warps' parts, segment by segment
+    // ---- join the warps' parts
     P* const mine = reinterpret_cast<P*>(slots) + blockIdx.x * 2;
-    auto finish = [&](const Segment& sg, int row, int c, float4 acc, float mm, float ll) {
-        const int32_t g = sg.sub / row_groups, r0 = (sg.sub - g * row_groups) * R;
-        if (r0 + row >= m.group || c >= m.d) return;
-        const int64_t h = (int64_t)sg.b * m.hq + g * m.group + r0 + row;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        store4(o + h * m.d + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-        if (c == 0) lse[h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * (1.f / kLog2e);
-    };
-    if (!skip) {
-        for (int i = 0; i < 2 * W;) {
-            const int64_t start = seg_of[i >> 1][i & 1];
-            if (start < 0) {
-                ++i;
-                continue;
+    int n_groups;
+    {
+        const int64_t of = lane < 2 * W ? seg_of[lane] : -1;
+        const uint32_t valid = __ballot_sync(0xffffffffu, of >= 0), below = valid & ((1u << lane) - 1);
+        const int64_t before = __shfl_sync(0xffffffffu, of, below ? 31 - __clz(below) : 0);
+        const uint32_t heads = __ballot_sync(0xffffffffu, of >= 0 && (!below || before != of));
+        n_groups = __popc(heads);
+        if (warp == 0 && of >= 0) list[__popc(below)] = lane;
+        for (int k = warp; k < n_groups; k += W) {
+            uint32_t rest = heads;
+            for (int i = 0; i < k; ++i) rest &= rest - 1;
+            const int first = __ffs(rest) - 1;
+            rest &= rest - 1;
+            const uint32_t set = valid & ~((1u << first) - 1) & (rest ? (rest & -rest) - 1 : ~0u);
+            const Segment sg = segment_at(L, __shfl_sync(0xffffffffu, of, first));
+            const bool here = sg.tile0() >= c_lo && sg.end() <= c_hi;
+            const int32_t g = sg.sub / row_groups, row0 = (sg.sub - g * row_groups) * R;
+            Group x;
+            x.first = __popc(valid & ((1u << first) - 1));
+            x.n = __popc(set);
+            x.rows = min(R, m.group - row0);
+            x.out = here ? -1 : sg.tile0() >= c_lo;
+            x.h = (int64_t)sg.b * m.hq + g * m.group + row0;
+            if (lane == 0) group[k] = x;
+            // Weights: a lane has one row of every (32 / R)-th part.
+            constexpr int kSub = 32 / R, kEach = (2 * W + kSub - 1) / kSub;
+            const int row = lane % R;
+            float pm[kEach], pl[kEach], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int at = i * kSub + lane / R;
+                const bool in = at < 2 * W && (set >> at & 1);
+                pm[i] = in ? part[at].m[row] : -INFINITY;
+                pl[i] = in ? part[at].l[row] : 0.f;
+                mm = fmaxf(mm, pm[i]);
             }
-            int n = i + 1;
-            while (n < 2 * W && (seg_of[n >> 1][n & 1] == start || seg_of[n >> 1][n & 1] < 0)) ++n;
-            const Segment sg = segment_at(L, start);
-            const bool whole = start >= c_lo && start + sg.tiles <= c_hi;
-            for (int x = tid; x < R * DP / 4; x += W * 32) {
-                const int row = x / (DP / 4), c = x % (DP / 4) * 4;
-                float mm = -INFINITY, ll = 0.f;
-                for (int k = i; k < n; ++k)
-                    if (seg_of[k >> 1][k & 1] >= 0) mm = fmaxf(mm, part[k].m[row]);
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = i; k < n; ++k) {
-                    if (seg_of[k >> 1][k & 1] < 0 || part[k].m[row] == -INFINITY) continue;
-                    const float w = ex2_approx(part[k].m[row] - mm);
-                    const float4 y = *reinterpret_cast<const float4*>(&part[k].o[row][c]);
-                    acc.x += w * y.x, acc.y += w * y.y, acc.z += w * y.z, acc.w += w * y.w;
-                    ll += w * part[k].l[row];
-                }
-                if (whole) {
-                    finish(sg, row, c, acc, mm, ll);
+#pragma unroll
+            for (int s = 16; s >= R; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, s));
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int at = i * kSub + lane / R;
+                const float w = pm[i] == -INFINITY ? 0.f : ex2_approx(pm[i] - mm);
+                if (at < 2 * W && (set >> at & 1)) weight[__popc(valid & ((1u << at) - 1))][row] = w;
+                ll += w * pl[i];
+            }
+#pragma unroll
+            for (int s = 16; s >= R; s >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, s);
+            if (lane < x.rows) {
+                if (here) {
+                    lse[x.h + row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * (1.f / kLog2e);
+                    scale_of[k][row] = ll == 0.f ? 0.f : 1.f / ll;
                 } else {
-                    P& out = mine[start >= c_lo];
-                    *reinterpret_cast<float4*>(&out.o[row][c]) = acc;
-                    if (c == 0) out.m[row] = mm, out.l[row] = ll;
+                    mine[x.out].m[row] = mm, mine[x.out].l[row] = ll;
                 }
             }
-            i = n;
+        }
+    }
+    __syncthreads();
+    for (int x = tid; x < n_groups * R * kCols; x += kThreads) {
+        const int k = x / (R * kCols), row = x / kCols % R, c = x % kCols * 4;
+        const Group gr = group[k];
+        if (row >= gr.rows) continue;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = gr.first; i < gr.first + gr.n; ++i) {
+            const float w = weight[i][row];
+            const float4 z = *reinterpret_cast<const float4*>(&part[list[i]].o[row][c]);
+            acc.x += w * z.x, acc.y += w * z.y, acc.z += w * z.z, acc.w += w * z.w;
+        }
+        if (gr.out >= 0) {
+            *reinterpret_cast<float4*>(&mine[gr.out].o[row][c]) = acc;
+        } else if (c < m.d) {
+            const float inv = scale_of[k][row];
+            store4(o + (gr.h + row) * m.d + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         }
     }
 
-    // ---- join the blocks' parts: side 0 is the segment that began in an earlier block, side 1 the one that goes on
-    Segment side[2];
-    bool open[2];
-    side[0] = segment_at(L, c_lo);
-    open[0] = side[0].start < c_lo;
-    side[1] = segment_at(L, c_hi - 1);
-    open[1] = side[1].start >= c_lo && side[1].start + side[1].tiles > c_hi;
-    if (!open[0] && !open[1]) return;
+    // ---- join the blocks' parts: the last block of a segment to arrive
+    if (side[0].n + side[1].n == 0) return;
     __threadfence();
     __syncthreads();
-    if (tid < 2) {
-        int32_t last = 0;
-        if (open[tid]) {
-            const int32_t first = L.part_of(side[tid].start), end = L.part_of(side[tid].start + side[tid].tiles - 1);
-            // Counts up to the number of blocks and wraps to 0 by itself: ready for the next call. A block that
-            // skipped its work for the status word's sake arrives all the same.
-            last = atomicInc(counters + first, end - first) == (uint32_t)(end - first);
-            __threadfence();
-        }
-        shared_flag[1 + tid] = last;
+    if (tid < 2 && side[tid].n) {
+        // Counts up to the number of blocks and wraps to 0 by itself: ready for the next call. A block that skipped
+        // its work for the status word's sake arrives all the same.
+        const uint32_t n = side[tid].n;
+        side[tid].last = atomicInc(counters + side[tid].first, n - 1) == n - 1 && !skip;
     }
     __syncthreads();
-    if (skip) return;
-    for (int s = 0; s < 2; ++s) {
-        if (!open[s] || !shared_flag[1 + s]) continue;
-        const int32_t first = L.part_of(side[s].start), end = L.part_of(side[s].start + side[s].tiles - 1);
-        const P* all = reinterpret_cast<const P*>(slots);
-        for (int x = tid; x < R * DP / 4; x += W * 32) {
-            const int row = x / (DP / 4), c = x % (DP / 4) * 4;
-            float mm = -INFINITY, ll = 0.f;
-            for (int k = first; k <= end; ++k) mm = fmaxf(mm, __ldcg(&all[2 * k + (k == first)].m[row]));
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = first; k <= end; ++k) {
-                const P& y = all[2 * k + (k == first)];
-                const float pm = __ldcg(&y.m[row]), pl = __ldcg(&y.l[row]);
-                const float4 z = __ldcg(reinterpret_cast<const float4*>(&y.o[row][c]));
-                const float w = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
-                acc.x += w * z.x, acc.y += w * z.y, acc.z += w * z.z, acc.w += w * z.w;
-                ll += w * pl;
-            }
-            finish(side[s], row, c, acc, mm, ll);
+    for (int sd = 0; sd < 2; ++sd) {
+        const Side S = side[sd];
+        if (!S.last) continue;
+        __threadfence();
+        // Block k's part; only the first block leaves the segment, the others entered it.
+        const P* all = reinterpret_cast<const P*>(slots) + 2 * S.first;
+        float* wt = reinterpret_cast<float*>(smem);  // [n][R]: maxima, then weights
+        float* ls = wt + kMaxParts * R;              // [n][R]: sums
+        float* inv = ls + kMaxParts * R;             // [R]
+        for (int x = tid; x < S.n * R; x += kThreads) {
+            const int k = x / R, row = x % R;
+            if (row >= S.rows) continue;
+            wt[x] = __ldcg(&all[2 * k + (k == 0)].m[row]);
+            ls[x] = __ldcg(&all[2 * k + (k == 0)].l[row]);
         }
+        __syncthreads();
+        for (int row = warp; row < S.rows; row += W) {
+            float mm = -INFINITY, ll = 0.f;
+            for (int k = lane; k < S.n; k += 32) mm = fmaxf(mm, wt[k * R + row]);
+#pragma unroll
+            for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+            for (int k = lane; k < S.n; k += 32) {
+                const float pm = wt[k * R + row], w = pm == -INFINITY ? 0.f : ex2_approx(pm - mm);
+                wt[k * R + row] = w;
+                ll += w * ls[k * R + row];
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x);
+            if (lane == 0) {
+                inv[row] = ll == 0.f ? 0.f : 1.f / ll;
+                lse[S.h + row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * (1.f / kLog2e);
+            }
+        }
+        __syncthreads();
+        for (int x = tid; x < S.rows * kCols; x += kThreads) {
+            const int row = x / kCols, c = x % kCols * 4;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < S.n; ++k) {
+                const float4 z = __ldcg(reinterpret_cast<const float4*>(&all[2 * k + (k == 0)].o[row][c]));
+                const float w = wt[k * R + row];
+                acc.x += w * z.x, acc.y += w * z.y, acc.z += w * z.z, acc.w += w * z.w;
+            }
+            const float i = inv[row];
+            if (c < m.d) store4(o + (S.h + row) * m.d + c, make_float4(acc.x * i, acc.y * i, acc.z * i, acc.w * i));
+        }
+        __syncthreads();  // the weights have been read
     }
 }
 
@@ -709,7 +824,7 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return note_error(e, "paged decode: device");
-    const size_t smem = sizeof(P) * W * 2 + sizeof(int32_t) * (m.n_seqs + 1);
+    const size_t smem = sizeof(P) * W * 2 + sizeof(int32_t) * std::max(m.n_seqs + 1, W * 36);
     auto kern = decode_kernel<T, DP, NT, W>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return note_error(e, "paged decode: shared memory");
