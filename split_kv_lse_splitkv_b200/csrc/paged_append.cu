@@ -1,10 +1,21 @@
 // Keys and values of new tokens into a paged cache, rotary positions applied on the way.
+//
+// One launch, bound by the bytes of the rows in and out. A lane holds two 16-byte pieces of a row whose channels are each
+// other's partners in the rotation, so it rotates them in registers; a warp takes several rows at once. The new keys
+// of a page and the bounds over the keys it holds are one block's work (the first token of the call in that page has
+// it): the block that rounds a key also has it for the minimum and maximum, keys that were there are read back, and no
+// two blocks write one page's bounds.
 #include <math.h>
+
+#include <algorithm>
 
 #include "paged.cuh"
 
 namespace splitkv {
 namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxPage = 1024;
 
 // Where token i goes. Padding and tokens out of range have page -1; the order is checked against the token
 // before it that is not padding.
@@ -33,7 +44,7 @@ __device__ T rotated(const AppendArgs& a, const T* x, int32_t i, const float* cs
     return from_f32<T>(second ? fmaf(w, c, u * s) : fmaf(u, c, -(w * s)));
 }
 
-// One block per token: queries, keys and values.
+// ---- any rope_dim: channels one by one. One block per token: queries, keys and values.
 template <typename T>
 __global__ void __launch_bounds__(128) append_rows_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     if (status_bad(status)) return;
@@ -85,10 +96,349 @@ __global__ void __launch_bounds__(128) append_bounds_kernel(PagedMeta m, AppendA
     }
 }
 
+// ---- rope_dim / 2 a multiple of 16 bytes: pieces of 16 bytes
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[8]) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    template <bool kMax>
+    static __device__ __forceinline__ uint32_t best(uint32_t x, uint32_t y) {
+        const __nv_bfloat162 u = *reinterpret_cast<__nv_bfloat162*>(&x), v = *reinterpret_cast<__nv_bfloat162*>(&y);
+        const __nv_bfloat162 r = kMax ? __hmax2(u, v) : __hmin2(u, v);
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    static constexpr uint32_t kInf = 0x7f807f80u, kNegInf = 0xff80ff80u;
+};
+template <>
+struct Vec<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[4]) {
+        f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    template <bool kMax>
+    static __device__ __forceinline__ uint32_t best(uint32_t x, uint32_t y) {
+        const float u = __uint_as_float(x), v = __uint_as_float(y);
+        return __float_as_uint(kMax ? fmaxf(u, v) : fminf(u, v));
+    }
+    static constexpr uint32_t kInf = 0x7f800000u, kNegInf = 0xff800000u;
+};
+
+template <typename T, bool kMax>
+__device__ __forceinline__ void take(uint4& x, const uint4& y) {
+    x.x = Vec<T>::template best<kMax>(x.x, y.x);
+    x.y = Vec<T>::template best<kMax>(x.y, y.y);
+    x.z = Vec<T>::template best<kMax>(x.z, y.z);
+    x.w = Vec<T>::template best<kMax>(x.w, y.w);
+}
+
+// How a row of d channels lies over lanes: `per_row` lanes a row, two pieces a lane.
+struct Lanes {
+    int per_row, rows;  // rows: how many a warp takes at once
+    int row, a, b;      // this lane's row (>= rows: none), first channels of its pieces (b < 0: only one)
+    int pair;           // first angle of its pairs, or -1: not rotated
+};
+
+template <typename T>
+__device__ __forceinline__ Lanes lanes_of(int d, int rope_dim, int interleaved, int lane) {
+    constexpr int kN = Vec<T>::kN;
+    const int turned = rope_dim / 2 / kN, rest = (d - rope_dim) / kN;
+    Lanes x;
+    x.per_row = turned + (rest + 1) / 2;
+    x.rows = 32 / x.per_row;
+    x.row = lane / x.per_row;
+    const int j = lane - x.row * x.per_row;
+    if (j < turned) {
+        x.a = interleaved ? 2 * j * kN : j * kN;
+        x.b = interleaved ? x.a + kN : rope_dim / 2 + x.a;
+        x.pair = j * kN;
+    } else {
+        x.a = rope_dim + 2 * (j - turned) * kN;
+        x.b = x.a + kN < d ? x.a + kN : -1;
+        x.pair = -1;
+    }
+    return x;
+}
+
+template <typename T>
+struct Angles {
+    float c[Vec<T>::kN], s[Vec<T>::kN];
+    __device__ __forceinline__ void load(const float* row, int half, int pair) {
+#pragma unroll
+        for (int i = 0; i < Vec<T>::kN; i += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(row + pair + i));
+            const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + pair + i));
+            c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+            s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+        }
+    }
+    // (x c - y s, y c + x s) for each pair (x, y), in float32, rounded once to the type.
+    __device__ __forceinline__ void turn(uint4& a, uint4& b, int interleaved) const {
+        constexpr int kN = Vec<T>::kN;
+        float x[kN], y[kN], u[kN], w[kN];
+        Vec<T>::unpack(a, x);
+        Vec<T>::unpack(b, y);
+        if (interleaved) {
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) {
+                u[2 * i] = fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i]));
+                u[2 * i + 1] = fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]);
+                w[2 * i] = fmaf(y[2 * i], c[kN / 2 + i], -(y[2 * i + 1] * s[kN / 2 + i]));
+                w[2 * i + 1] = fmaf(y[2 * i + 1], c[kN / 2 + i], y[2 * i] * s[kN / 2 + i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                u[i] = fmaf(x[i], c[i], -(y[i] * s[i]));
+                w[i] = fmaf(y[i], c[i], x[i] * s[i]);
+            }
+        }
+        a = Vec<T>::pack(u);
+        b = Vec<T>::pack(w);
+    }
+};
+
+__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// Queries of one token: heads [h0, h1), a warp.
+template <typename T>
+__device__ __forceinline__ void append_queries(const PagedMeta& m, const AppendArgs& a, int64_t i, int h0, int h1,
+                                               int lane, int32_t* status) {
+    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    const int32_t seq = __ldg(a.token_seq + i), pos = __ldg(a.token_pos + i);
+    // A token that is out of range is reported with its keys; its queries pass as they are.
+    const bool turn = L.pair >= 0 && seq >= 0 && pos >= 0 && pos < a.rope_len;
+    Angles<T> ang;
+    if (turn) ang.load(a.rope + (int64_t)pos * a.rope_dim, a.rope_dim / 2, L.pair);
+    const T* src = (const T*)a.q + i * a.q_stride;
+    T* dst = (T*)a.q_out + i * m.hq * m.d;
+    if (L.row >= L.rows) return;
+    constexpr int kAhead = 4;
+    for (int h = h0 + L.row; h < h1; h += kAhead * L.rows) {
+        uint4 x[kAhead], y[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = (int64_t)(h + k * L.rows) * m.d;
+            if (h + k * L.rows >= h1) continue;
+            x[k] = ldg16(src + at + L.a);
+            if (L.b >= 0) y[k] = ldg16(src + at + L.b);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = (int64_t)(h + k * L.rows) * m.d;
+            if (h + k * L.rows >= h1) continue;
+            if (turn) ang.turn(x[k], y[k], a.interleaved);
+            *reinterpret_cast<uint4*>(dst + at + L.a) = x[k];
+            if (L.b >= 0) *reinterpret_cast<uint4*>(dst + at + L.b) = y[k];
+        }
+    }
+}
+
+// Blocks [0, kv_blocks): the keys and values of the pages whose first token of the call is one of the block's
+// `slice` tokens. Blocks from there on: queries, `heads` of a token per warp.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArgs a, int32_t* status, int64_t kv_blocks,
+                                                          int32_t slice, int32_t heads) {
+    constexpr int kN = Vec<T>::kN;
+    __shared__ int32_t tokens[kMaxPage];      // the page's new tokens, from the first one on
+    __shared__ uint32_t is_new[kMaxPage / 32];
+    __shared__ int32_t n_tokens, last_pos;
+    __shared__ uint4 red[kWarps][32][4];      // minima and maxima of a lane's two pieces
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (__syncthreads_or(status_bad(status))) return;
+
+    if (blockIdx.x >= kv_blocks) {
+        const int32_t per_token = (m.hq + heads - 1) / heads;
+        const int64_t unit = (blockIdx.x - kv_blocks) * kWarps + warp, i = unit / per_token;
+        const int32_t h0 = (int32_t)(unit - i * per_token) * heads;
+        if (i < a.n_tokens) append_queries<T>(m, a, i, h0, min(h0 + heads, m.hq), lane, status);
+        return;
+    }
+
+    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    const int v_row = m.d / kN, v_rows = 32 / v_row;  // values: a lane per piece
+    // Which of the slice's tokens are the first of a page: a lane per token, the same in every warp.
+    const int64_t i0 = blockIdx.x * (int64_t)slice;
+    uint32_t firsts;
+    {
+        const int64_t i = i0 + lane;
+        const bool mine = lane < slice && i < a.n_tokens;
+        const int32_t seq = mine ? __ldg(a.token_seq + i) : -1, pos = seq >= 0 ? __ldg(a.token_pos + i) : 0;
+        bool first = seq >= 0;
+        if (first) {
+            int32_t before = -1, before_pos = -1;
+            for (int64_t p = i - 1; p >= 0; --p)  // padding passed over
+                if ((before = __ldg(a.token_seq + p)) >= 0) {
+                    before_pos = __ldg(a.token_pos + p);
+                    break;
+                }
+            if (warp == 0 && (before > seq || (before == seq && before_pos >= pos)))
+                raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
+            if (seq >= m.n_seqs || pos < 0 || pos >= (int64_t)m.max_pages * m.page || (a.rope && pos >= a.rope_len)) {
+                if (warp == 0) raise_status(status, SPLITKV_DEV_BAD_TOKEN);
+                first = false;
+            } else if (before == seq && before_pos >= 0 && before_pos >> m.page_shift == pos >> m.page_shift) {
+                first = false;
+            }
+        }
+        firsts = __ballot_sync(0xffffffffu, first);
+    }
+    for (; firsts; firsts &= firsts - 1) {
+        // Every thread of the block takes the same way.
+        const int64_t i = i0 + __ffs(firsts) - 1;
+        const int32_t seq = __ldg(a.token_seq + i), entry = __ldg(a.token_pos + i) >> m.page_shift;
+        const int32_t page = paged_page(m, a.table + seq * m.table_stride, entry, status);
+        if (page < 0) continue;
+
+        // The page's tokens: from here to the first token of another page.
+        __syncthreads();  // the previous page is done with shared memory
+        if (tid == 0) n_tokens = 0, last_pos = 0;
+        for (int x = tid; x < (m.page + 31) / 32; x += kThreads) is_new[x] = 0;
+        __syncthreads();
+        for (int64_t base = i;; base += kThreads) {
+            const int64_t t = base + tid;
+            const int32_t s = t < a.n_tokens ? __ldg(a.token_seq + t) : INT32_MAX;
+            const int32_t q = s >= 0 && s < INT32_MAX ? __ldg(a.token_pos + t) : -1;
+            const bool in = s == seq && q >= 0 && q >> m.page_shift == entry && !(a.rope && q >= a.rope_len);
+            const uint32_t stops = __ballot_sync(0xffffffffu, s >= 0 && !in);
+            // The first thread that sees another page's token ends the run; later tokens of this page (out of order) are
+            // somebody else's.
+            __shared__ int32_t stop;
+            if (tid == 0) stop = kThreads;
+            __syncthreads();
+            if (lane == 0 && stops) atomicMin(&stop, warp * 32 + __ffs(stops) - 1);
+            __syncthreads();
+            const int32_t end = stop;
+            if (in && tid < end) {
+                const int32_t k = atomicAdd(&n_tokens, 1), off = q & (m.page - 1);
+                if (k < kMaxPage) tokens[k] = (int32_t)(t - i);
+                atomicOr(&is_new[off >> 5], 1u << (off & 31));
+                atomicMax(&last_pos, off);
+            }
+            __syncthreads();
+            if (end < kThreads) break;
+        }
+        const int32_t n = min(n_tokens, kMaxPage), last = last_pos;
+
+        // Tasks: kv head, and where there are fewer heads than warps a share of the rows.
+        const int32_t subs = max(1, kWarps / m.hkv);
+        for (int32_t task0 = 0; task0 < m.hkv * subs; task0 += kWarps) {
+            const int32_t task = task0 + warp, g = task / subs, sub = task - g * subs;
+            const bool work = task < m.hkv * subs;
+            uint4 lo[2], hi[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                lo[x] = make_uint4(Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf);
+                hi[x] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
+            }
+            T* kc = (T*)a.k_cache + paged_row(m, page, work ? g : 0, 0);
+            T* vc = (T*)a.v_cache + paged_row(m, page, work ? g : 0, 0);
+            if (work && L.row < L.rows) {
+                for (int32_t k = sub * L.rows + L.row; k < n; k += subs * L.rows) {
+                    const int64_t t = i + tokens[k];
+                    const int32_t q = __ldg(a.token_pos + t);
+                    const T* src = (const T*)a.k + t * a.k_stride + g * m.d;
+                    uint4 x = ldg16(src + L.a), y = make_uint4(0, 0, 0, 0);
+                    if (L.b >= 0) y = ldg16(src + L.b);
+                    if (L.pair >= 0) {
+                        Angles<T> ang;
+                        ang.load(a.rope + (int64_t)q * a.rope_dim, a.rope_dim / 2, L.pair);
+                        ang.turn(x, y, a.interleaved);
+                    }
+                    T* dst = kc + (q & (m.page - 1)) * m.token_stride;
+                    *reinterpret_cast<uint4*>(dst + L.a) = x;
+                    take<T, false>(lo[0], x), take<T, true>(hi[0], x);
+                    if (L.b >= 0) {
+                        *reinterpret_cast<uint4*>(dst + L.b) = y;
+                        take<T, false>(lo[1], y), take<T, true>(hi[1], y);
+                    }
+                }
+                if (a.k_bounds) {
+#pragma unroll 4
+                    for (int32_t off = sub * L.rows + L.row; off < last; off += subs * L.rows) {
+                        if (is_new[off >> 5] >> (off & 31) & 1) continue;
+                        const T* src = kc + off * m.token_stride;
+                        const uint4 x = *reinterpret_cast<const uint4*>(src + L.a);
+                        take<T, false>(lo[0], x), take<T, true>(hi[0], x);
+                        if (L.b >= 0) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(src + L.b);
+                            take<T, false>(lo[1], y), take<T, true>(hi[1], y);
+                        }
+                    }
+                }
+            }
+            if (work && lane < v_rows * v_row) {
+                const int c = lane % v_row * kN;
+                for (int32_t k = sub * v_rows + lane / v_row; k < n; k += subs * v_rows) {
+                    const int64_t t = i + tokens[k];
+                    const int32_t off = __ldg(a.token_pos + t) & (m.page - 1);
+                    *reinterpret_cast<uint4*>(vc + off * m.token_stride + c) =
+                        ldg16((const T*)a.v + t * a.v_stride + g * m.d + c);
+                }
+            }
+            if (!a.k_bounds) continue;
+            red[warp][lane][0] = lo[0], red[warp][lane][1] = lo[1], red[warp][lane][2] = hi[0], red[warp][lane][3] = hi[1];
+            __syncthreads();
+            // The first warp of a head joins the head's lanes: a thread per (minimum or maximum, piece of a row).
+            if (work && sub == 0) {
+                const int32_t warps = min(subs, m.hkv * subs - task);
+                for (int x = lane; x < 2 * L.per_row; x += 32) {
+                    const bool top = x >= L.per_row;
+                    const int j = top ? x - L.per_row : x;
+                    const Lanes J = lanes_of<T>(m.d, a.rope_dim, a.interleaved, j);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int c = half ? J.b : J.a;
+                        if (c < 0) continue;
+                        uint4 best = red[warp][j][half + (top ? 2 : 0)];
+                        for (int w = 0; w < warps; ++w)
+                            for (int r = 0; r < L.rows; ++r) {
+                                const uint4 y = red[warp + w][r * L.per_row + j][half + (top ? 2 : 0)];
+                                if (top) take<T, true>(best, y); else take<T, false>(best, y);
+                            }
+                        *reinterpret_cast<uint4*>((T*)a.k_bounds + (((int64_t)page * m.hkv + g) * 2 + top) * m.d + c) = best;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
 template <typename T>
 cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
-    append_rows_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
-    if (a.k_bounds) append_bounds_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+    if (a.rope_dim / 2 % Vec<T>::kN) {
+        append_rows_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+        if (a.k_bounds) append_bounds_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+        return note_error(cudaGetLastError(), "paged append");
+    }
+    constexpr int kSms = 148;
+    // A block per token while there are few; then as many tokens a block as leave several blocks per SM.
+    const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens / (kSms * 4)));
+    const int64_t kv_blocks = (a.n_tokens + slice - 1) / slice;
+    const int turned = a.rope_dim / 2 / Vec<T>::kN, rows = 32 / (turned + ((m.d - a.rope_dim) / Vec<T>::kN + 1) / 2);
+    int32_t heads = std::min(m.hq, a.n_tokens * m.hq / rows < kSms * 32 ? rows : 4 * rows);
+    const int64_t q_blocks = a.q ? (a.n_tokens * ((m.hq + heads - 1) / heads) + kWarps - 1) / kWarps : 0;
+    append_kernel<T><<<(unsigned)(kv_blocks + q_blocks), kThreads, 0, st>>>(m, a, status, kv_blocks, slice, heads);
     return note_error(cudaGetLastError(), "paged append");
 }
 

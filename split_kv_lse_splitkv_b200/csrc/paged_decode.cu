@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     const int row_groups = (m.group + R - 1) / R;
 
     // ---- the line of units
-    const bool skip = status_bad(status);
+    const bool skip = __any_sync(0xffffffffu, status_bad(status));
     auto units_of = [&](int b) {
         const int32_t len = paged_len(m, seq_len, b, status);
         int32_t n = len;
