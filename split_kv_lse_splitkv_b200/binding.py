@@ -311,29 +311,37 @@ def splitkv_paged_workspace_size(paged: Paged, n_seqs: int) -> int:
     return int(_lib.splitkv_paged_workspace_size(ctypes.byref(paged), int(n_seqs)))
 
 
+def _at(t):
+    # A plain integer: these calls are made once per layer and token, where a wrapper object per argument is felt.
+    return None if t is None else t.data_ptr()
+
+
+def _on(stream) -> int:
+    return stream if type(stream) is int else _stream(stream).value or 0
+
+
 def splitkv_paged_append(paged, n_seqs, n_tokens, q, q_stride, k, k_stride, v, v_stride, rope, rope_dim, rope_len,
                          interleaved, page_table, token_seq, token_pos, q_out, k_cache, v_cache, k_bounds, status,
                          stream=None):
-    _check(_lib.splitkv_paged_append(ctypes.byref(paged), int(n_seqs), int(n_tokens), _p(q), int(q_stride), _p(k),
-                                     int(k_stride), _p(v), int(v_stride), _p(rope), int(rope_dim), int(rope_len),
-                                     int(interleaved), _p(page_table), _p(token_seq), _p(token_pos), _p(q_out),
-                                     _p(k_cache), _p(v_cache), _p(k_bounds), _p(status), _stream(stream)),
-           "splitkv_paged_append")
+    _check(_lib.splitkv_paged_append(paged, n_seqs, n_tokens, _at(q), q_stride, _at(k), k_stride, _at(v), v_stride,
+                                     _at(rope), rope_dim, rope_len, interleaved, _at(page_table), _at(token_seq),
+                                     _at(token_pos), _at(q_out), _at(k_cache), _at(v_cache), _at(k_bounds),
+                                     _at(status), _on(stream)), "splitkv_paged_append")
 
 
 def splitkv_paged_decode(paged, n_seqs, q, q_stride, k_cache, v_cache, page_table, seq_len, pages, n_select, o, lse,
                          status, workspace, stream=None):
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.splitkv_paged_decode(ctypes.byref(paged), int(n_seqs), _p(q), int(q_stride), _p(k_cache), _p(v_cache),
-                                     _p(page_table), _p(seq_len), _p(pages), int(n_select), _p(o), _p(lse), _p(status),
-                                     _p(workspace), nbytes, _stream(stream)), "splitkv_paged_decode")
+    _check(_lib.splitkv_paged_decode(paged, n_seqs, _at(q), q_stride, _at(k_cache), _at(v_cache), _at(page_table),
+                                     _at(seq_len), _at(pages), n_select, _at(o), _at(lse), _at(status),
+                                     _at(workspace), nbytes, _on(stream)), "splitkv_paged_decode")
 
 
 def splitkv_paged_select(paged, n_seqs, q, q_stride, k_bounds, page_table, seq_len, n_select, keep_first, keep_last,
                          pages, status, stream=None):
-    _check(_lib.splitkv_paged_select(ctypes.byref(paged), int(n_seqs), _p(q), int(q_stride), _p(k_bounds),
-                                     _p(page_table), _p(seq_len), int(n_select), int(keep_first), int(keep_last),
-                                     _p(pages), _p(status), _stream(stream)), "splitkv_paged_select")
+    _check(_lib.splitkv_paged_select(paged, n_seqs, _at(q), q_stride, _at(k_bounds), _at(page_table), _at(seq_len),
+                                     n_select, keep_first, keep_last, _at(pages), _at(status), _on(stream)),
+           "splitkv_paged_select")
 
 
 # ------------------------------------------------------------------ convenience: the whole path

@@ -407,6 +407,31 @@ SPLITKV_API int splitkv_attn_bwd_rank(const splitkv_problem* problem, const void
 }
 
 // ------------------------------------------------------------------ paged cache
+namespace splitkv {
+
+cudaError_t sm_count(int* sms) {
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return note_error(e, "cudaGetDevice");
+    if (dev < kMaxDevices && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < kMaxDevices) known[dev].store(*sms, std::memory_order_relaxed);
+    return note_error(e, "cudaDeviceGetAttribute");
+}
+
+cudaError_t allow_smem(const void* kernel, size_t most, SmemGrants& granted) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return note_error(e, "cudaGetDevice");
+    if (dev < kMaxDevices && granted[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess && dev < kMaxDevices) granted[dev].store(true, std::memory_order_relaxed);
+    return note_error(e, "cudaFuncSetAttribute");
+}
+
+}  // namespace splitkv
+
 namespace {
 
 // Fill `m` from a host description and a number of sequences; returns SPLITKV_OK or a negative code.

@@ -2,6 +2,8 @@
 // geometry by value, row addressing and the internal launcher declarations.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace splitkv {
@@ -49,6 +51,12 @@ cudaError_t launch_paged_select(const PagedMeta& m, const void* q, int64_t q_str
                                 const int32_t* table, const int32_t* seq_len, int32_t n_select, int32_t keep_first,
                                 int32_t keep_last, int32_t* pages, int32_t* status, cudaStream_t st);
 constexpr int32_t kMaxSelectPages = SPLITKV_PAGED_MAX_SELECT_PAGES;
+
+// SMs of the current device, and the opt-in to the `most` bytes of dynamic shared memory that a kernel is ever launched
+// with (`granted`: a static of the caller's for that kernel). Both are asked of the runtime once per device.
+cudaError_t sm_count(int* sms);
+using SmemGrants = std::atomic<bool>[kMaxDevices];
+cudaError_t allow_smem(const void* kernel, size_t most, SmemGrants& granted);
 
 // Length of sequence b, or 0 (with the status bit) when it is not in [0, max_pages * page].
 __device__ __forceinline__ int32_t paged_len(const PagedMeta& m, const int32_t* seq_len, int32_t b, int32_t* status) {

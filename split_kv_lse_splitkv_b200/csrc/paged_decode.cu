@@ -820,14 +820,14 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
                    const int32_t* table, const int32_t* seq_len, const int32_t* pages, int32_t n_select, void* o,
                    float* lse, int32_t* status, void* ws, cudaStream_t st) {
     using P = Partial<DP, 8 * NT>;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return note_error(e, "paged decode: device");
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     const size_t smem = sizeof(P) * W * 2 + sizeof(int32_t) * std::max(m.n_seqs + 1, W * 36);
     auto kern = decode_kernel<T, DP, NT, W>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return note_error(e, "paged decode: shared memory");
+    static SmemGrants granted;
+    e = allow_smem((const void*)kern, sizeof(P) * W * 2 + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), granted);
+    if (e != cudaSuccess) return e;
     const int grid = std::min(sms, kMaxParts);
     kern<<<grid, W * 32, smem, st>>>(m, (const T*)q, q_stride, (const T*)k_cache, (const T*)v_cache, table, seq_len,
                                      pages, n_select, (T*)o, lse, status, (uint32_t*)ws, (char*)ws + kCounterBytes);

@@ -314,10 +314,9 @@ template <typename T, int LP, int NC>
 cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_bounds, const int32_t* table,
                    const int32_t* seq_len, int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t* pages,
                    int32_t* status, cudaStream_t st) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return note_error(e, "paged select: device");
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     // Blocks a row: as many as its scores need room for, then until the blocks fill the GPU twice, while each keeps
     // 128 pages.
     const int64_t rows = (int64_t)m.n_seqs * m.hkv;
@@ -327,8 +326,9 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
         cl *= 2;
     auto kern = select_kernel<T, LP, NC>;
     const size_t smem = sizeof(uint64_t) * ((m.max_pages + cl - 1) / cl);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)std::max<size_t>(smem, 1024));
-    if (e != cudaSuccess) return note_error(e, "paged select: shared memory");
+    static SmemGrants granted;
+    e = allow_smem((const void*)kern, sizeof(uint64_t) * kMaxShare, granted);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rows * cl));
     cfg.blockDim = dim3(kThreads);

@@ -14,6 +14,12 @@ from . import binding as B
 from .binding import EINVAL, SplitKVError
 
 _COUNTERS = 4096  # bytes at the head of the workspace that have to be zero before its first use
+_MOST = (1 << 31) - 1
+
+# torch.cuda.current_device() and current_stream(device).cuda_stream, without the objects around them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def rope_table(n_positions: int, rope_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -91,7 +97,7 @@ class PagedKV:
             self._ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
             self._stream = torch.cuda.current_stream(self.device)
 
-    # -- marshalling
+    # -- marshalling (texts are made only where a check fails: these calls are made once per layer and token)
     def _layout(self, width: int, stride: int) -> B.Paged:
         got = self._layouts.get((width, stride))
         if got is None:
@@ -102,52 +108,48 @@ class PagedKV:
                 self._layouts[(width, stride)] = got
         return got
 
-    def _on(self, fn, stream, *args, **kw):
-        """fn(*args, **kw) with the cache's device current, on `stream` where one is given."""
+    def _on(self, fn, stream, *args):
+        """fn(*args) with the cache's device current, on `stream` where one is given."""
         if self._index is None:
             raise SplitKVError(EINVAL, f"PagedKV: the cache is on {self.device}, not on a CUDA device")
         if stream is None:
             with torch.cuda.device(self._index):
-                return fn(*args, **kw)
+                return fn(*args)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.device)
         _need(stream.device == self.device, "PagedKV: a stream of another device than the cache's")
         with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-
-    def _away(self) -> bool:
-        return self._index is None or torch._C._cuda_getDevice() != self._index
-
-    def _raw(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self._index)
+            return fn(*args)
 
     def _table(self, page_table, what):
-        _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.device == self.device and
-              (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-              f"{what}: page_table must be an int32 [n_seqs, pages] tensor on the cache's device, its rows dense")
+        if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != self.device or
+                (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+            raise SplitKVError(EINVAL, f"{what}: page_table must be an int32 [n_seqs, pages] tensor on the cache's "
+                               "device, its rows dense")
         n, width = page_table.shape
-        _need(n <= self.max_seqs and 1 <= width <= self.max_pages,
-              f"{what}: a page table of {n} x {width}, made for up to {self.max_seqs} x {self.max_pages}")
         stride = page_table.stride(0) if n > 1 else width
-        _need(stride >= width, f"{what}: page_table's rows overlap")
+        if n > self.max_seqs or not 1 <= width <= self.max_pages or stride < width:
+            raise SplitKVError(EINVAL, f"{what}: a page table of {n} x {width}, {stride} apart; made for up to "
+                               f"{self.max_seqs} x {self.max_pages}, apart")
         return n, self._layout(width, stride)
 
     def _list(self, t, n, what, name):
-        _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.device == self.device and
-              (n <= 1 or t.stride(0) == 1), f"{what}: {name} must be a dense int32 [{n}] tensor on the cache's device")
+        if t.dtype != torch.int32 or t.shape != (n,) or t.device != self.device or not t.is_contiguous():
+            raise SplitKVError(EINVAL, f"{what}: {name} must be a dense int32 [{n}] tensor on the cache's device")
 
     def _rows(self, t, n, shape, what, name) -> int:
         """Stride between the tokens of a [n, heads, head_dim] tensor whose heads are dense."""
-        st = t.stride()
-        _need(t.dtype == self.dtype and t.dim() == 3 and t.shape[0] == n and t.shape[1:] == shape and
-              t.device == self.device and st[2] == 1 and (shape[0] == 1 or st[1] == shape[1]),
-              f"{what}: {name} must be a {self.dtype} [{n}, {shape[0]}, {shape[1]}] tensor on the cache's device, each "
-              "token's heads dense")
-        return st[0] if n > 1 else shape[0] * shape[1]
+        heads, d = shape
+        if t.dtype == self.dtype and t.shape == (n, heads, d) and t.device == self.device:
+            st = t.stride()
+            if st[2] == 1 and (heads == 1 or st[1] == d):
+                return st[0] if n > 1 else heads * d
+        raise SplitKVError(EINVAL, f"{what}: {name} must be a {self.dtype} [{n}, {heads}, {d}] tensor on the cache's "
+                           "device, each token's heads dense")
 
     def _out(self, t, shape, dtype, what, name):
-        _need(tuple(t.shape) == shape and t.dtype == dtype and t.device == self.device and t.is_contiguous(),
-              f"{what}: {name} must be a dense {dtype} tensor of {shape} on the cache's device")
+        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+            raise SplitKVError(EINVAL, f"{what}: {name} must be a dense {dtype} tensor of {shape} on the cache's device")
 
     # -- the calls
     def append(self, k, v, page_table, token_seq, token_pos, q=None, rope: Optional[torch.Tensor] = None,
@@ -164,22 +166,24 @@ class PagedKV:
         vs = self._rows(v, n, self._kv_shape, what, "v")
         self._list(token_seq, n, what, "token_seq")
         self._list(token_pos, n, what, "token_pos")
-        qs = 0 if q is None else self._rows(q, n, self._q_shape, what, "q")
-        rope_len = rope_dim = 0
+        qs = rope_len = rope_dim = 0
         if rope is not None:
-            _need(rope.dtype == torch.float32 and rope.dim() == 2 and rope.device == self.device and
-                  rope.is_contiguous(), f"{what}: rope must be a dense float32 [positions, rope_dim] tensor")
+            if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != self.device or not rope.is_contiguous():
+                raise SplitKVError(EINVAL, f"{what}: rope must be a dense float32 [positions, rope_dim] tensor")
             rope_len, rope_dim = rope.shape
-        _need(q is not None or q_out is None, f"{what}: q_out without q")
+        if q is not None:
+            qs = self._rows(q, n, self._q_shape, what, "q")
+        elif q_out is not None:
+            raise SplitKVError(EINVAL, f"{what}: q_out without q")
         if q_out is not None:
             self._out(q_out, (n, *self._q_shape), self.dtype, what, "q_out")
-        if stream is not None or self._away():
+        if stream is not None or self._index is None or _current_device() != self._index:
             return self._on(self.append, stream, k, v, page_table, token_seq, token_pos, q, rope, interleaved, q_out)
         if q is not None and q_out is None:
-            q_out = torch.empty((n, *self._q_shape), dtype=self.dtype, device=self.device)
-        B.splitkv_paged_append(layout, n_seqs, n, q, qs, k, ks, v, vs, rope, rope_dim, rope_len, interleaved,
+            q_out = q.new_empty((n, *self._q_shape))
+        B.splitkv_paged_append(layout, n_seqs, n, q, qs, k, ks, v, vs, rope, rope_dim, rope_len, 1 if interleaved else 0,
                                page_table, token_seq, token_pos, q_out, self.k_cache, self.v_cache, self.k_bounds,
-                               self.status, self._raw())
+                               self.status, _raw_stream(self._index))
         return q_out
 
     def select(self, q, page_table, seq_lens, n_select, keep_first=1, keep_last=1, pages=None, stream=None):
@@ -187,20 +191,25 @@ class PagedKV:
         the new token of each sequence reads at each kv head, ascending, then -1. The first ``keep_first`` and last
         ``keep_last`` pages are always among them, the others are those with the largest bound on their scores."""
         what = "PagedKV.select"
-        _need(self.k_bounds is not None, f"{what}: the cache has no bounds (PagedKV(..., bounds=True))")
+        if self.k_bounds is None:
+            raise SplitKVError(EINVAL, f"{what}: the cache has no bounds (PagedKV(..., bounds=True))")
         n, layout = self._table(page_table, what)
         qs = self._rows(q, n, self._q_shape, what, "q")
         self._list(seq_lens, n, what, "seq_lens")
         n_select = int(n_select)
-        _need(n_select >= 1 and keep_first >= 0 and keep_last >= 0, f"{what}: n_select, keep_first, keep_last")
+        if n_select < 1 or keep_first < 0 or keep_last < 0:
+            raise SplitKVError(EINVAL, f"{what}: n_select, keep_first, keep_last")
+        shape = (n, self.n_kv_heads, n_select)
         if pages is not None:
-            self._out(pages, (n, self.n_kv_heads, n_select), torch.int32, what, "pages")
-        if stream is not None or self._away():
+            self._out(pages, shape, torch.int32, what, "pages")
+        if stream is not None or self._index is None or _current_device() != self._index:
             return self._on(self.select, stream, q, page_table, seq_lens, n_select, keep_first, keep_last, pages)
         if pages is None:
-            pages = torch.empty((n, self.n_kv_heads, n_select), dtype=torch.int32, device=self.device)
-        B.splitkv_paged_select(layout, n, q, qs, self.k_bounds, page_table, seq_lens, n_select, keep_first, keep_last,
-                               pages, self.status, self._raw())
+            pages = seq_lens.new_empty(shape)
+        # No sequence has more pages than its row: any larger number says the same.
+        B.splitkv_paged_select(layout, n, q, qs, self.k_bounds, page_table, seq_lens, n_select,
+                               min(int(keep_first), _MOST), min(int(keep_last), _MOST), pages, self.status,
+                               _raw_stream(self._index))
         return pages
 
     def decode(self, q, page_table, seq_lens, pages=None, o=None, lse=None, stream=None):
@@ -215,19 +224,21 @@ class PagedKV:
         n_select = 0
         if pages is not None:
             n_select = pages.shape[2] if pages.dim() == 3 else 0
-            _need(n_select >= 1, f"{what}: pages must be [n_seqs, n_kv_heads, n_select]")
+            if n_select < 1:
+                raise SplitKVError(EINVAL, f"{what}: pages must be [n_seqs, n_kv_heads, n_select]")
             self._out(pages, (n, self.n_kv_heads, n_select), torch.int32, what, "pages")
         if o is not None:
             self._out(o, (n, *self._q_shape), self.dtype, what, "o")
         if lse is not None:
             self._out(lse, (n, self.n_q_heads), torch.float32, what, "lse")
-        if stream is not None or self._away():
+        index = self._index
+        if stream is not None or index is None or _current_device() != index:
             return self._on(self.decode, stream, q, page_table, seq_lens, pages, o, lse)
         if o is None:
-            o = torch.empty((n, *self._q_shape), dtype=self.dtype, device=self.device)
+            o = q.new_empty((n, *self._q_shape))
         if lse is None:
-            lse = torch.empty((n, self.n_q_heads), dtype=torch.float32, device=self.device)
-        raw = self._raw()
+            lse = q.new_empty((n, self.n_q_heads), dtype=torch.float32)
+        raw = _raw_stream(index)
         if torch._C._cuda_isCurrentStreamCapturing():
             # The graph may be replayed beside other work of this object: scratch of its own, its counters zeroed
             # by the graph.
