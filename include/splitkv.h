@@ -434,12 +434,14 @@ int splitkv_paged_decode(const splitkv_paged *paged, int32_t n_seqs, const void 
  * those with the highest scores; equal scores go to the lower page. The sum is formed as on the left, in float64: a
  * bound that is infinite or NaN (0 * inf) may make it NaN, which counts as the lowest score. The first
  * pages go before the last ones where n_select does not hold both. max_pages is at most
- * SPLITKV_PAGED_MAX_SELECT_PAGES (EUNSUPPORTED beyond).
+ * SPLITKV_PAGED_MAX_SELECT_PAGES (EUNSUPPORTED beyond). workspace_d: splitkv_paged_select_workspace_size() bytes of
+ * scratch (8 per page, kv head and sequence), written before it is read; calls that share it must be ordered.
  */
+size_t splitkv_paged_select_workspace_size(const splitkv_paged *paged, int32_t n_seqs);
 int splitkv_paged_select(const splitkv_paged *paged, int32_t n_seqs, const void *q, int64_t q_stride,
                          const void *k_bounds, const int32_t *page_table_d, const int32_t *seq_len_d,
                          int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t *pages_d,
-                         int32_t *status_d, void *stream);
+                         int32_t *status_d, void *workspace_d, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,8 @@ that decodes token by token (:func:`splitkv_paged_append`, :func:`splitkv_paged_
 _EXPORTS = (
     "DEV_ANCHOR_ORDER", "DEV_ANCHOR_RANGE", "DEV_BAD_COST", "DEV_BAD_PLAN", "DEV_SMEM_ALIGN", "DEV_TIMEOUT", "FWD_DEFAULT", "FWD_SIMT",
     "DEV_BAD_LENGTH", "DEV_BAD_PAGE", "DEV_BAD_TOKEN", "DEV_TOKEN_ORDER", "PagedKV", "make_paged", "rope_table",
-    "splitkv_paged_append", "splitkv_paged_decode", "splitkv_paged_select", "splitkv_paged_workspace_size",
+    "splitkv_paged_append", "splitkv_paged_decode", "splitkv_paged_select", "splitkv_paged_select_workspace_size",
+    "splitkv_paged_workspace_size",
     "FWD_TEST_STARVE",
     "LIB_PATH", "SplitKV", "SplitKVError", "make_problem", "splitkv_attn_bwd", "splitkv_attn_fwd", "splitkv_cost",
     "splitkv_last_error", "splitkv_lse_merge", "splitkv_max_workers", "splitkv_cp_plan", "splitkv_cost_rank",

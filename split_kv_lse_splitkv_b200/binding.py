@@ -104,7 +104,8 @@ _SIGS = {
                              + [_vp] * 9),
     "splitkv_paged_decode": (_i32, [_PG, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz,
                                     _vp]),
-    "splitkv_paged_select": (_i32, [_PG, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "splitkv_paged_select": (_i32, [_PG, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "splitkv_paged_select_workspace_size": (_sz, [_PG, _i32]),
 }
 EXPORTS = tuple(_SIGS)
 for _name, (_res, _args) in _SIGS.items():
@@ -337,10 +338,16 @@ def splitkv_paged_decode(paged, n_seqs, q, q_stride, k_cache, v_cache, page_tabl
                                      _at(workspace), nbytes, _on(stream)), "splitkv_paged_decode")
 
 
+def splitkv_paged_select_workspace_size(paged: Paged, n_seqs: int) -> int:
+    return int(_lib.splitkv_paged_select_workspace_size(ctypes.byref(paged), int(n_seqs)))
+
+
 def splitkv_paged_select(paged, n_seqs, q, q_stride, k_bounds, page_table, seq_len, n_select, keep_first, keep_last,
-                         pages, status, stream=None):
+                         pages, status, workspace, stream=None):
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.splitkv_paged_select(paged, n_seqs, _at(q), q_stride, _at(k_bounds), _at(page_table), _at(seq_len),
-                                     n_select, keep_first, keep_last, _at(pages), _at(status), _on(stream)),
+                                     n_select, keep_first, keep_last, _at(pages), _at(status), _at(workspace), nbytes,
+                                     _on(stream)),
            "splitkv_paged_select")
 
 

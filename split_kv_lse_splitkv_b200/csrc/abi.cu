@@ -492,6 +492,12 @@ SPLITKV_API size_t splitkv_paged_workspace_size(const splitkv_paged* paged, int3
     return build_paged(paged, n_seqs, &m) ? 0 : paged_decode_workspace(m);
 }
 
+SPLITKV_API size_t splitkv_paged_select_workspace_size(const splitkv_paged* paged, int32_t n_seqs) {
+    PagedMeta m;
+    if (build_paged(paged, n_seqs, &m) || m.max_pages > kMaxSelectPages) return 0;
+    return std::max<size_t>(paged_select_workspace(m), 16);
+}
+
 SPLITKV_API int splitkv_paged_append(const splitkv_paged* paged, int32_t n_seqs, int64_t n_tokens, const void* q,
                                      int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                                      const float* rope, int32_t rope_dim, int64_t rope_len, int32_t interleaved,
@@ -549,7 +555,7 @@ SPLITKV_API int splitkv_paged_decode(const splitkv_paged* paged, int32_t n_seqs,
 SPLITKV_API int splitkv_paged_select(const splitkv_paged* paged, int32_t n_seqs, const void* q, int64_t q_stride,
                                      const void* k_bounds, const int32_t* page_table_d, const int32_t* seq_len_d,
                                      int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t* pages_d,
-                                     int32_t* status_d, void* stream) {
+                                     int32_t* status_d, void* workspace_d, size_t workspace_bytes, void* stream) {
     clear_error();
     PagedMeta m;
     int rc = build_paged(paged, n_seqs, &m);
@@ -560,6 +566,8 @@ SPLITKV_API int splitkv_paged_select(const splitkv_paged* paged, int32_t n_seqs,
     if (!rows_ok(m, q, n_seqs, q_stride, m.hq) || !k_bounds || !page_table_d || !seq_len_d || !pages_d)
         return SPLITKV_EINVAL;
     if (!aligned16(k_bounds)) return SPLITKV_EINVAL;
+    if (!workspace_d || workspace_bytes < paged_select_workspace(m)) return SPLITKV_ENOSPACE;
+    if (!aligned16(workspace_d)) return SPLITKV_EINVAL;
     return cuda_status(launch_paged_select(m, q, q_stride, k_bounds, page_table_d, seq_len_d, n_select, keep_first,
-                                           keep_last, pages_d, status_d, (cudaStream_t)stream));
+                                           keep_last, pages_d, status_d, workspace_d, (cudaStream_t)stream));
 }

@@ -49,7 +49,8 @@ size_t paged_decode_workspace(const PagedMeta& m);
 
 cudaError_t launch_paged_select(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_bounds,
                                 const int32_t* table, const int32_t* seq_len, int32_t n_select, int32_t keep_first,
-                                int32_t keep_last, int32_t* pages, int32_t* status, cudaStream_t st);
+                                int32_t keep_last, int32_t* pages, int32_t* status, void* ws, cudaStream_t st);
+size_t paged_select_workspace(const PagedMeta& m);
 constexpr int32_t kMaxSelectPages = SPLITKV_PAGED_MAX_SELECT_PAGES;
 
 // SMs of the current device, and the opt-in to the `most` bytes of dynamic shared memory that a kernel is ever launched
@@ -80,6 +81,21 @@ __device__ __forceinline__ int32_t paged_page(const PagedMeta& m, const int32_t*
 
 __device__ __forceinline__ int64_t paged_row(const PagedMeta& m, int64_t page, int32_t g, int32_t off) {
     return page * m.page_stride + g * m.head_stride + off * m.token_stride;
+}
+
+// 16 bytes that are read once, or zeros. Predicated rather than branched around (a branch per load cost more than the
+// load), and volatile: the loads stay where they are issued, ahead of the work that hides them (the compiler would move
+// them down to their use).
+__device__ __forceinline__ uint4 ldg_stream_if(const void* p, bool in) {
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+        : "l"(p), "r"((int)in));
+    return r;
 }
 
 }  // namespace splitkv

@@ -35,14 +35,6 @@ constexpr int kMaxDP = 128, kMaxRows = 16;
 
 static_assert(kMaxParts * sizeof(uint32_t) <= kCounterBytes, "counters");
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
-}
-
 // D += A B for one 16x8 tile, bf16 x bf16 -> f32 (16 deep) or tf32 x tf32 -> f32 (8 deep).
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -117,7 +109,7 @@ struct Frag<__nv_bfloat16, DP, NT> {
 #pragma unroll
             for (int j = 0; j < DP / 32; ++j) {
                 const int c = 32 * j + 8 * t;
-                k[j][x] = in && c < d ? ldg_stream(kc + off + c) : make_uint4(0, 0, 0, 0);
+                k[j][x] = ldg_stream_if(kc + off + c, in && c < d);
             }
         }
     }
@@ -131,7 +123,7 @@ struct Frag<__nv_bfloat16, DP, NT> {
 #pragma unroll
             for (int c0 = 0; c0 < DP / 64; ++c0) {
                 const int c = 64 * c0 + 8 * g;
-                v[c0][x] = in && c < d ? ldg_stream(vc + off + c) : make_uint4(0, 0, 0, 0);
+                v[c0][x] = ldg_stream_if(vc + off + c, in && c < d);
             }
         }
     }
@@ -203,8 +195,8 @@ struct Frag<float, DP, NT> {
     float4 v[DP / 32][4];
     float o[NT][kOut][4];
 
-    static __device__ __forceinline__ float4 load(const T* p) {
-        const uint4 r = ldg_stream(p);
+    static __device__ __forceinline__ float4 load(const T* p, bool in) {
+        const uint4 r = ldg_stream_if(p, in);
         return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
     }
     __device__ __forceinline__ void load_q(const T* base, int rows, int d, int lane) {
@@ -228,7 +220,7 @@ struct Frag<float, DP, NT> {
 #pragma unroll
             for (int j = 0; j < DP / 16; ++j) {
                 const int c = 16 * j + 4 * t;
-                k[j][x] = in && c < d ? load(kc + off + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                k[j][x] = load(kc + off + c, in && c < d);
             }
         }
     }
@@ -241,7 +233,7 @@ struct Frag<float, DP, NT> {
 #pragma unroll
             for (int c0 = 0; c0 < DP / 32; ++c0) {
                 const int c = 32 * c0 + 4 * g;
-                v[c0][x] = in && c < d ? load(vc + off + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[c0][x] = load(vc + off + c, in && c < d);
             }
         }
     }

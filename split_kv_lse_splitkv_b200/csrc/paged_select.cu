@@ -1,13 +1,17 @@
 // Selection of the pages that a sequence's new token reads, by a bound on its scores.
 //
 // A page scores sum_i a_i kmax_i + b_i kmin_i with a_i, b_i the sums of the positive and negative query channels of the kv
-// head's group: one dot product of 2d terms for the whole group, bound by the bytes of the bounds. It is formed in
-// float64 (bf16 or float32 channels enter exactly, the order of the sum moves it by 1e-16), so that which page comes
-// in does not hang on a rounding. A cluster of blocks shares a (sequence, kv head): each block scores a run of pages
-// and keeps their scores in shared memory as ordered integers; the n-th largest is found by counting into 2048 bins
-// over the range that is left (the first pass spans the scores' own range, so two passes nearly always decide), the
-// blocks adding up each other's bins through distributed shared memory; then each writes its pages in order.
-#include <cooperative_groups.h>
+// head's group: one dot product of 2d terms for the whole group, bound by the bytes of the bounds. Which page comes in
+// is to follow the float64 score, so that no rounding decides it; formed in float64 for every page it would be bound by
+// its instructions (3.5 a channel). So every page is scored in float32 with a bound on the error, and only pages that
+// float32 cannot tell from the n-th largest are scored again in float64 (a page or two of thousands; where there are
+// many, as among equal pages, all of them).
+//
+// Two kernels. The first scores: all pages of all (sequence, kv head) rows form one line, cut evenly over the warps of
+// all SMs, because one SM draws at most ~45 GB/s from DRAM however much it has in flight (a cluster of blocks per row
+// left most SMs idle in a ragged batch: 32 sequences of 100 .. 65536 keys took 50 .. 114 us). The second has a block per
+// row: it counts the scores into 2048 bins over their own range to find the bin of the n-th largest, ranks that bin's
+// few pages one by one and writes the pages in order.
 #include <math.h>
 
 #include <algorithm>
@@ -17,14 +21,13 @@
 namespace splitkv {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits;
-constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 8;        // loads of bounds a lane has in flight
-constexpr int kMaxShare = 16384;  // pages of one block: 128 KB of scores
-static_assert(kMaxShare * kMaxCluster >= kMaxSelectPages, "the longest sequence fits a cluster");
+constexpr int kLoads = 8;         // loads of bounds a lane has in flight, and again as many for the round after
+constexpr int kInShared = 16384;  // scores that the second kernel keeps in shared memory; longer rows stay in L2
+constexpr int kCands = 512;       // pages that are ranked one by one
+constexpr int kWords = 512, kSpan = kWords * 32;
+static_assert(kWords == kThreads && kCands <= kThreads, "one word, one candidate a thread");
 
 // The order of the scores as unsigned integers: larger score, larger key, all above 0. NaN: below every number.
 __device__ __forceinline__ uint64_t score_key(double s) {
@@ -32,326 +35,534 @@ __device__ __forceinline__ uint64_t score_key(double s) {
     const uint64_t u = (uint64_t)__double_as_longlong(s + 0.0);  // -0 ranks as 0
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
+__device__ __forceinline__ uint32_t score_key(float s) {
+    if (s != s) return 1;
+    const uint32_t u = __float_as_uint(s + 0.f);
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_score(uint32_t u) { return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u); }
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
 
+// The channels in 16 bytes of bounds or queries, exact in float32.
 template <typename T>
-struct Chunk;  // 16 bytes of bounds
+struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
     static constexpr int kN = 8;
-    static __device__ __forceinline__ double dot(const uint4& x, const double (&c)[8]) {
+    static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[8]) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s = fma((double)__uint_as_float(w[i] << 16), c[2 * i], s);
-            s = fma((double)__uint_as_float(w[i] & 0xffff0000u), c[2 * i + 1], s);
-        }
-        return s;
+        for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 };
 template <>
 struct Chunk<float> {
     static constexpr int kN = 4;
-    static __device__ __forceinline__ double dot(const uint4& x, const double (&c)[4]) {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma((double)__uint_as_float(w[i]), c[i], s);
-        return s;
+    static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[4]) {
+        f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
     }
 };
 
-// What the blocks of a cluster read of each other.
-struct Shared {
-    uint32_t hist[kBins];
-    uint64_t least, most;   // keys of this block
-    int32_t skip, above, equal;
+// How many pages of a sequence have to be scored, and which are taken without: pages < lead and >= tail.
+struct Row {
+    int32_t count, want, lead, tail;
+    bool scored;
 };
+__device__ __forceinline__ Row row_of(const PagedMeta& m, int32_t len, int32_t n_select, int32_t keep_first,
+                                      int32_t keep_last) {
+    Row r;
+    r.count = (len + m.page - 1) >> m.page_shift;
+    r.want = min(n_select, r.count);
+    r.lead = min(keep_first, r.count);
+    r.tail = max(r.count - keep_last, r.lead);
+    r.scored = r.count > n_select && r.lead + r.count - r.tail < r.want;
+    return r;
+}
 
+// ---- first kernel: {key of the float32 score (0: not ranked), bound on the sum of its terms' sizes} of every page.
 // LP lanes hold the 2d channels of one page, NC chunks of 16 bytes each.
 template <typename T, int LP, int NC>
-__global__ void __launch_bounds__(kThreads) select_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
-                                                          const T* __restrict__ bounds,
-                                                          const int32_t* __restrict__ table,
-                                                          const int32_t* __restrict__ seq_len, int32_t n_select,
-                                                          int32_t keep_first, int32_t keep_last,
-                                                          int32_t* __restrict__ pages, int32_t* status, int32_t cl) {
-    constexpr int kN = Chunk<T>::kN, kPer = 32 / LP;  // pages a warp reads with one load a lane
-    extern __shared__ uint64_t keys[];                // of this block's pages; 0: not ranked
-    __shared__ Shared sh;
-    __shared__ double coef[256];
-    __shared__ uint64_t red[2 * kWarps];
-    __shared__ int32_t ired[2 * kWarps];
-    __shared__ int32_t found[3];
-    cg::cluster_group cluster = cg::this_cluster();
+__global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
+                                                         const T* __restrict__ bounds,
+                                                         const int32_t* __restrict__ table,
+                                                         const int32_t* __restrict__ seq_len, int32_t n_select,
+                                                         int32_t keep_first, int32_t keep_last, uint2* __restrict__ scores,
+                                                         int32_t* status) {
+    constexpr int kN = Chunk<T>::kN, kPer = 32 / LP;    // pages a warp reads with one load a lane
+    constexpr int kV = kLoads / NC, kStep = kV * kPer;  // pages of a lane's round, of a warp's
+    static_assert(kStep <= 32 && LP >= kV, "one table entry, one result a lane");
+    extern __shared__ int32_t prefix_all[];  // pages to score of the sequences before b
+    int32_t* prefix = prefix_all;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = blockIdx.x % cl, row = blockIdx.x / cl, b = row / m.hkv, g = row % m.hkv;
-
-    if (tid == 0) sh.skip = status_bad(status);
-    const int32_t len = paged_len(m, seq_len, b, status);
-    const int32_t count = (len + m.page - 1) >> m.page_shift, want = min(n_select, count);
-    const int32_t lead = min(keep_first, count), tail = max(count - keep_last, lead);  // always taken: < lead, >= tail
-    int32_t* out = pages + (int64_t)row * n_select;
-    if (count <= n_select || lead + count - tail >= want) {  // no score decides (the same for the whole cluster)
-        for (int i = rank * kThreads + tid; i < n_select; i += cl * kThreads)
-            out[i] = i >= want ? -1 : count <= n_select || i < lead ? i : tail + i - lead;
-        for (int i = rank * kThreads + tid; i < count; i += cl * kThreads)  // the pages are checked all the same
-            paged_page(m, table + b * m.table_stride, i, status);
-        return;
-    }
-
-    // ---- scores of pages [p0, p1)
-    for (int i = tid; i < m.d; i += kThreads) {
-        double up = 0.0, down = 0.0;
-        const T* x = q + b * q_stride + (int64_t)g * m.group * m.d + i;
-        for (int h = 0; h < m.group; ++h) {
-            const double y = to_f32<T>(x[(int64_t)h * m.d]);
-            up += y > 0.0 ? y : 0.0;
-            down += y < 0.0 ? y : 0.0;
-            if (y != y) up = down = y;
+    if (__any_sync(0xffffffffu, status_bad(status)) && m.n_seqs <= 32) return;
+    auto pages_of = [&](int b) {
+        const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
+        return r.scored ? r.count : 0;
+    };
+    if (m.n_seqs <= 32) {  // each warp by itself
+        int32_t x = lane < m.n_seqs ? pages_of(lane) : 0;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, x, s);
+            if (lane >= s) x += y;
         }
-        coef[i] = down;
-        coef[m.d + i] = up;
+        prefix += warp * 36;
+        prefix[lane + 1] = x;
+        if (lane == 0) prefix[0] = 0;
+        __syncwarp();
+    } else {
+        for (int b = tid; b < m.n_seqs; b += kThreads) prefix[b + 1] = pages_of(b);
+        __syncthreads();
+        if (warp == 0) {
+            int32_t carry = 0;
+            for (int b0 = 0; b0 < m.n_seqs; b0 += 32) {
+                int32_t x = b0 + lane < m.n_seqs ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int32_t y = __shfl_up_sync(0xffffffffu, x, s);
+                    if (lane >= s) x += y;
+                }
+                if (b0 + lane < m.n_seqs) prefix[b0 + lane + 1] = carry + x;
+                carry += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) prefix[0] = 0;
+        }
+        __syncthreads();
     }
-    const int32_t share = (count + cl - 1) / cl, p0 = min(rank * share, count), n = min(share, count - p0);
-    const int32_t* trow = table + b * m.table_stride + p0;
-    __syncthreads();
+    const int64_t total = (int64_t)prefix[m.n_seqs] * m.hkv;
+    const int32_t n_warps = gridDim.x * kWarps, me = warp * gridDim.x + blockIdx.x;  // neighbours on other SMs
+    const int64_t per = max((total + n_warps - 1) / n_warps, (int64_t)kStep);
+    const int64_t u_end = min((me + 1) * per, total);
     const int sub = lane % LP, at = lane / LP;  // the lane's part of a page, its page of the kPer
-    double c[NC][kN];
-#pragma unroll
-    for (int k = 0; k < NC; ++k)
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int e = (k * LP + sub) * kN + i;
-            c[k][i] = e < 2 * m.d ? coef[e] : 0.0;
+    const int64_t page_step = (int64_t)m.hkv * 2 * m.d;
+
+    for (int64_t u = me * per; u < u_end;) {
+        // The rest of this warp's share of one (sequence, kv head): pages [p, p_end).
+        int32_t b = 0;
+        for (int32_t hi = m.n_seqs; hi - b > 1;) {
+            const int32_t mid = (b + hi) >> 1;
+            if ((int64_t)prefix[mid] * m.hkv <= u) b = mid; else hi = mid;
         }
-    uint64_t least = ~0ull, most = 0;
-    constexpr int kStep = kUnroll / NC * kPer;  // pages of a warp's round: kStep <= 32
-    static_assert(kStep <= 32, "one table entry a lane");
-    for (int32_t base = warp * kStep; base < n; base += kWarps * kStep) {
-        const int32_t mine = lane < kStep && base + lane < n ? paged_page(m, trow, base + lane, status) : -1;
-        uint4 x[kUnroll / NC][NC];
+        const int32_t count = prefix[b + 1] - prefix[b];
+        const int64_t rem = u - (int64_t)prefix[b] * m.hkv;
+        const int32_t g = (int32_t)(rem / count);
+        int32_t p = (int32_t)(rem - (int64_t)g * count);
+        const int32_t p_end = (int32_t)min((int64_t)count, p + (u_end - u));
+        u += p_end - p;
+        const int32_t* trow = table + b * m.table_stride;
+        const T* head = bounds + (int64_t)g * 2 * m.d;
+        uint2* out = scores + ((int64_t)b * m.hkv + g) * m.max_pages;
+
+        auto entry = [&](int32_t p) { return lane < kStep && p + lane < p_end ? paged_page(m, trow, p + lane, status) : -1; };
+        auto load = [&](int32_t mine, uint4 (&x)[kV][NC]) {
 #pragma unroll
-        for (int u = 0; u < kUnroll / NC; ++u) {
-            const int32_t page = __shfl_sync(0xffffffffu, mine, u * kPer + at);
+            for (int v = 0; v < kV; ++v) {
+                const int32_t page = __shfl_sync(0xffffffffu, mine, v * kPer + at);
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const int e = (k * LP + sub) * kN;
+                    x[v][k] = ldg_stream_if(head + page * page_step + e, page >= 0 && e < 2 * m.d);
+                }
+            }
+        };
+        // The next round's bounds are on their way during a round, the table's entries one round more.
+        int32_t mine = entry(p), next = entry(p + kStep);
+        float c[NC][kN] = {};
+        for (int h0 = 0; h0 < m.group; h0 += 4)
 #pragma unroll
             for (int k = 0; k < NC; ++k) {
-                const int e = (k * LP + sub) * kN;
-                x[u][k] = page >= 0 && e < 2 * m.d
-                              ? __ldg(reinterpret_cast<const uint4*>(bounds + ((int64_t)page * m.hkv + g) * 2 * m.d + e))
-                              : make_uint4(0, 0, 0, 0);
+                const int e = (k * LP + sub) * kN, i = e < m.d ? e : e - m.d;  // kmin's channels first, then kmax's
+                uint4 y[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    y[h] = ldg_stream_if(q + b * q_stride + (int64_t)(g * m.group + h0 + h) * m.d + i,
+                                         e < 2 * m.d && h0 + h < m.group);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    float f[kN];
+                    Chunk<T>::unpack(y[h], f);
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) c[k][j] += (e < m.d) != (f[j] > 0.f) ? f[j] : 0.f;  // (NaN: into one of them)
+                }
             }
-        }
-        double s[kUnroll / NC];
+        uint4 x[kV][NC], ahead[kV][NC];
+        load(mine, x);
+        for (;;) {
+            const int32_t after = entry(p + 2 * kStep);
+            load(next, ahead);
+            float s[kV], size = 0.f;
 #pragma unroll
-        for (int u = 0; u < kUnroll / NC; ++u) {
-            s[u] = 0.0;
+            for (int v = 0; v < kV; ++v) {
+                float terms = 0.f;
+                s[v] = 0.f;
 #pragma unroll
-            for (int k = 0; k < NC; ++k) s[u] += Chunk<T>::dot(x[u][k], c[k]);
-        }
-        // Sums over the LP lanes; halving the values at each step while there are several: lane `sub` ends up
-        // with the sum of value (sub * values / LP), the lanes of a value side by side.
-        constexpr int kV = kUnroll / NC;
+                for (int k = 0; k < NC; ++k) {
+                    float f[kN];
+                    Chunk<T>::unpack(x[v][k], f);
 #pragma unroll
-        for (int step = LP / 2, have = kV; step; step >>= 1) {
-            if (have > 1) {
-                have >>= 1;
-#pragma unroll
-                for (int i = 0; i < kV / 2; ++i)
-                    if (i < have) {
-                        const double give = sub & step ? s[i] : s[i + have], keep = sub & step ? s[i + have] : s[i];
-                        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, step);
+                    for (int j = 0; j < kN; ++j) {
+                        const float y = f[j] * c[k][j];
+                        s[v] += y, terms += fabsf(y);
                     }
-            } else {
-                s[0] += __shfl_xor_sync(0xffffffffu, s[0], step);
+                }
+                size = max_nan(size, terms);
             }
-        }
-        static_assert(LP >= kV, "every value of a round gets a lane");
-        const int u = sub / (LP / kV);
-        const int32_t p = base + u * kPer + at;
-        const int32_t page = __shfl_sync(0xffffffffu, mine, (u * kPer + at) & 31);
-        if (sub % (LP / kV) == 0 && p < n) {
-            const bool kept = p0 + p < lead || p0 + p >= tail;
-            const uint64_t key = kept || page < 0 ? 0 : score_key(s[0]);
-            keys[p] = key;
-            if (key) least = min(least, key), most = max(most, key);
-        }
-    }
-
-    // ---- the scores' range
+            // Sums over the LP lanes; halving the values at each step while there are several: lane `sub` ends up
+            // with the sum of value (sub * values / LP), the lanes of a value side by side.
 #pragma unroll
-    for (int x = 16; x; x >>= 1) {
-        least = min(least, __shfl_xor_sync(0xffffffffu, least, x));
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+            for (int step = LP / 2, have = kV; step; step >>= 1) {
+                size += __shfl_xor_sync(0xffffffffu, size, step);
+                if (have > 1) {
+                    have >>= 1;
+#pragma unroll
+                    for (int i = 0; i < kV / 2; ++i)
+                        if (i < have) {
+                            const float give = sub & step ? s[i] : s[i + have], keep = sub & step ? s[i + have] : s[i];
+                            s[i] = keep + __shfl_xor_sync(0xffffffffu, give, step);
+                        }
+                } else {
+                    s[0] += __shfl_xor_sync(0xffffffffu, s[0], step);
+                }
+            }
+            const int v = sub / (LP / kV), mine_at = v * kPer + at;
+            const int32_t page = __shfl_sync(0xffffffffu, mine, mine_at & 31);
+            if (sub % (LP / kV) == 0 && p + mine_at < p_end) {
+                const int32_t at_p = p + mine_at;
+                const bool kept = at_p < keep_first || at_p >= count - keep_last;
+                out[at_p] = make_uint2(kept || page < 0 ? 0 : score_key(s[0]), __float_as_uint(size));
+            }
+            if ((p += kStep) >= p_end) break;
+            mine = next, next = after;
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+#pragma unroll
+                for (int k = 0; k < NC; ++k) x[v][k] = ahead[v][k];
+        }
     }
-    if (lane == 0) red[warp] = least, red[kWarps + warp] = most;
+}
+
+// ---- second kernel
+
+struct Shared {
+    uint32_t hist[kBins];
+    uint64_t cand_key[kCands];
+    int32_t cand_page[kCands];
+    uint64_t red[2 * kWarps];
+    int32_t ired[kWarps];
+    int32_t found[4];
+    uint32_t in_mask[kWords], eq_mask[kWords];
+};
+
+// Sum of x over the threads before this one; `all`: over every thread. Two barriers.
+__device__ __noinline__ int2 sum_before(int32_t x, int32_t* warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t incl = x;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += y;
+    }
+    if (lane == 31) warps[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-        least = lane < kWarps ? red[lane] : ~0ull;
-        most = lane < kWarps ? red[kWarps + lane] : 0;
-#pragma unroll
-        for (int x = 8; x; x >>= 1) {
-            least = min(least, __shfl_xor_sync(0xffffffffu, least, x));
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
-        }
-        if (lane == 0) sh.least = least, sh.most = most;
-    }
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-    cluster.sync();
-    const int skip = cluster.map_shared_rank(&sh, 0)->skip;  // one block's word decides for all of them
-    uint64_t lo = ~0ull, hi = 0;
-    for (int r = 0; r < cl; ++r) {
-        const Shared* x = cluster.map_shared_rank(&sh, r);
-        lo = min(lo, x->least);
-        hi = max(hi, x->most);
-    }
-    if (skip || lo > hi) {  // nothing ranked: every page in use is out of range
-        cluster.sync();
-        return;
-    }
+    const int32_t w = lane < kWarps ? warps[lane] : 0;
+    const int32_t below = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0), all = __reduce_add_sync(0xffffffffu, w);
+    __syncthreads();
+    return make_int2(below + incl - x, all);
+}
 
-    // ---- the `need` largest keys: [lo, hi] is narrowed to the bin that holds the last of them
-    int32_t need = want - (lead + count - tail), in_bin = 0;
+// The keys of a row, of one width or the other.
+template <typename K>
+struct Keys {
+    K* at;
+    int32_t n, step;  // elements from one page's key to the next's
+    template <typename F>
+    __device__ __forceinline__ void each(F&& fn) const {  // pages over the threads
+#pragma unroll 4
+        for (int32_t p = threadIdx.x; p < n; p += kThreads) fn(p, at[(int64_t)p * step]);
+    }
+};
+
+// Narrows [lo, hi], which holds all keys of interest, to a bin with the `need`-th largest of them; `need` then counts
+// from the bin's top. Ends with at most kCands keys in the bin, or with all of them needed, or all equal. hist is zero
+// before and after.
+template <typename K>
+__device__ __noinline__ void narrow(const Keys<K>& keys, Shared& sh, uint64_t& lo, uint64_t& hi, int32_t& need,
+                                    int32_t& in_bin) {
+    const int tid = threadIdx.x;
     const uint64_t range = hi - lo;
-    int shift = range >> kBits ? 64 - kBits - __clzll((long long)range) : 0;
+    int shift = lo < hi && range >> kBits ? 64 - kBits - __clzll((long long)range) : 0;
     for (;;) {
-        for (int i = tid; i < n; i += kThreads) {
-            const uint64_t k = keys[i];
+        if (tid < 4) sh.found[tid] = 0;
+        __syncthreads();
+        keys.each([&](int32_t, K k) {
             if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
-        }
-        cluster.sync();
+        });
+        __syncthreads();
         // Thread t has the bins 4t .. 4t + 3 counted from the top.
         constexpr int kEach = kBins / kThreads;
-        uint32_t v[kEach] = {};
-        for (int r = 0; r < cl; ++r) {
-            const uint32_t* x = cluster.map_shared_rank(&sh, r)->hist + kBins - kEach * (tid + 1);
-            const uint4 y = *reinterpret_cast<const uint4*>(x);
-            v[0] += y.w, v[1] += y.z, v[2] += y.y, v[3] += y.x;
-        }
         static_assert(kEach == 4, "one 16-byte load");
-        int32_t sum = v[0] + v[1] + v[2] + v[3], incl = sum;
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, incl, x);
-            if (lane >= x) incl += y;
-        }
-        if (lane == 31) ired[warp] = incl;
-        if (tid == 0) found[0] = 0, found[1] = 0, found[2] = 0;
-        __syncthreads();
-        int32_t above = incl - sum;
-        for (int w = 0; w < warp; ++w) above += ired[w];
+        uint4* bins = reinterpret_cast<uint4*>(sh.hist + kBins - kEach * (tid + 1));
+        const uint4 y = *bins;
+        *bins = make_uint4(0, 0, 0, 0);
+        const uint32_t v[kEach] = {y.w, y.z, y.y, y.x};
+        const int32_t sum = v[0] + v[1] + v[2] + v[3];
+        int32_t above = sum_before(sum, sh.ired).x;
         if (above < need && above + sum >= need) {
             int k = 0;
             while (above + (int32_t)v[k] < need) above += v[k++];
-            found[0] = kBins - 1 - kEach * tid - k;
-            found[1] = above;
-            found[2] = v[k];
+            sh.found[0] = kBins - 1 - kEach * tid - k;
+            sh.found[1] = above;
+            sh.found[2] = v[k];
         }
-        cluster.sync();  // the bins have been read, by all
-        need -= found[1];
-        in_bin = found[2];
-        lo += (uint64_t)found[0] << shift;
-        hi = lo + ((1ull << shift) - 1);
-        if (in_bin <= need || shift == 0) break;
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+        __syncthreads();
+        need -= sh.found[1];
+        in_bin = sh.found[2];
+        lo += (uint64_t)sh.found[0] << shift;
+        const uint64_t width = (1ull << shift) - 1;
+        if (hi - lo > width) hi = lo + width;  // (the last bin may reach past the range)
+        __syncthreads();
+        if (in_bin <= kCands || in_bin <= need || shift == 0) return;
         shift = max(0, shift - kBits);
-        __syncthreads();
     }
-    // Taken: kept pages, keys above hi, and of those in [lo, hi] all, or (equal keys then) the first `need`.
-    const bool ties = in_bin > need;
-    int32_t n_above = 0, n_equal = 0;
-    for (int i = tid; i < n; i += kThreads) {
-        const bool kept = p0 + i < lead || p0 + i >= tail;
-        n_above += kept || keys[i] > hi;
-        n_equal += !kept && keys[i] >= lo && keys[i] <= hi;
+}
+
+// Smallest and largest of the threads' values.
+__device__ __noinline__ void range_of(Shared& sh, uint64_t& lo, uint64_t& hi) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+    for (int x = 16; x; x >>= 1) {
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, x));
     }
-    n_above = __reduce_add_sync(0xffffffffu, n_above);
-    n_equal = __reduce_add_sync(0xffffffffu, n_equal);
-    if (lane == 0) ired[warp] = n_above, ired[kWarps + warp] = n_equal;
+    if (lane == 0) sh.red[warp] = lo, sh.red[kWarps + warp] = hi;
     __syncthreads();
-    if (tid == 0) {
-        n_above = n_equal = 0;
-        for (int w = 0; w < kWarps; ++w) n_above += ired[w], n_equal += ired[kWarps + w];
-        sh.above = n_above, sh.equal = n_equal;
+    lo = sh.red[lane % kWarps], hi = sh.red[kWarps + lane % kWarps];
+#pragma unroll 1
+    for (int x = kWarps / 2; x; x >>= 1) {
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, x));
     }
-    cluster.sync();
-    int32_t at_out = 0, eq_before = 0;  // results and equal keys of the blocks before this one
-    for (int r = 0; r < rank; ++r) {
-        const Shared* x = cluster.map_shared_rank(&sh, r);
-        const int32_t e = x->equal;
-        at_out += x->above + (ties ? max(0, min(e, need - eq_before)) : e);
-        eq_before += e;
+    __syncthreads();
+}
+
+// The keys in [from, to] into the list of candidates; how many there are (those past kCands are only counted).
+template <typename K>
+__device__ __noinline__ int32_t gather(const Keys<K>& keys, Shared& sh, uint64_t from, uint64_t to) {
+    if (threadIdx.x == 0) sh.found[3] = 0;
+    __syncthreads();
+    keys.each([&](int32_t p, K k) {
+        if (k >= from && k <= to) {
+            const int32_t i = atomicAdd(&sh.found[3], 1);
+            if (i < kCands) sh.cand_key[i] = k, sh.cand_page[i] = p;
+        }
+    });
+    __syncthreads();
+    return sh.found[3];
+}
+
+// How many of the n candidates come before this thread's: larger keys, equal keys of lower pages.
+__device__ __forceinline__ int32_t place(const Shared& sh, int32_t n) {
+    const uint64_t k = sh.cand_key[threadIdx.x];
+    const int32_t p = sh.cand_page[threadIdx.x];
+    int32_t better = 0;
+    for (int j = 0; j < n; ++j) better += sh.cand_key[j] > k || (sh.cand_key[j] == k && sh.cand_page[j] < p);
+    return better;
+}
+
+// The key of page p's float64 score, on one warp: the group's query channels again, in float64.
+template <typename T>
+__device__ __noinline__ uint64_t exact(const PagedMeta& m, const T* q, const T* head, const int32_t* trow, int32_t p,
+                                       int32_t* status) {
+    const int lane = threadIdx.x & 31;
+    const int32_t page = paged_page(m, trow, p, status);
+    if (page < 0) return 0;
+    const T* x = head + page * ((int64_t)m.hkv * 2 * m.d);
+    double s = 0.0;
+    for (int i = lane; i < m.d; i += 32) {
+        double up = 0.0, down = 0.0;
+        for (int h = 0; h < m.group; ++h) {
+            const double y = to_f32<T>(q[(int64_t)h * m.d + i]);
+            up += y >= 0.0 ? y : y != y ? y : 0.0;
+            down += y <= 0.0 ? y : y != y ? y : 0.0;
+        }
+        s = fma((double)to_f32<T>(x[i]), down, s);
+        s = fma((double)to_f32<T>(x[m.d + i]), up, s);
     }
-    cluster.sync();  // nobody reads this block's memory from here on
-    for (int32_t base = 0; base < n; base += kThreads) {
-        const int32_t i = base + tid;
-        const bool kept = i < n && (p0 + i < lead || p0 + i >= tail);
-        const uint64_t k = i < n ? keys[i] : 0;
-        const bool sure = kept || (i < n && k > hi), equal = i < n && !kept && k >= lo && k <= hi;
-        const uint32_t se = __ballot_sync(0xffffffffu, sure), ee = __ballot_sync(0xffffffffu, equal);
-        if (lane == 0) ired[warp] = __popc(se), ired[kWarps + warp] = __popc(ee);
-        __syncthreads();
-        int32_t eq = eq_before, sures = 0, eq_all = 0, sures_all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) eq += eq_all, sures = sures_all;
-            eq_all += ired[kWarps + w];
-            sures_all += ired[w];
+#pragma unroll
+    for (int y = 16; y; y >>= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
+    return score_key(s);
+}
+
+// Writes the pages taken, in order: the kept ones, those with keys >= take, and of those in [lo, hi] the first `ties`.
+template <typename K>
+__device__ __noinline__ void write_pages(const Keys<K>& keys, Shared& sh, const Row& r, uint64_t take, uint64_t lo,
+                                         uint64_t hi, int32_t ties, int32_t* out, int32_t n_select) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t at_out = 0, left = ties;
+    for (int32_t first = 0; first < r.count; first += kSpan) {
+        const int32_t here = min(r.count - first, kSpan);
+        for (int32_t i = warp * 32; i < here; i += kThreads) {
+            const int32_t p = first + i + lane;
+            const uint64_t key = p < r.count ? keys.at[(int64_t)p * keys.step] : 0;
+            const bool kept = p < r.count && (p < r.lead || p >= r.tail);
+            const uint32_t in = __ballot_sync(0xffffffffu, kept || (key && key >= take));
+            const uint32_t eq = __ballot_sync(0xffffffffu, ties && key >= lo && key <= hi);
+            if (lane == 0) sh.in_mask[i / 32] = in, sh.eq_mask[i / 32] = eq;
         }
-        const uint32_t lt = (1u << lane) - 1;
-        const int32_t eq_mine = eq + __popc(ee & lt);  // equal keys before this page
-        const int32_t take = ties ? need : INT32_MAX;
-        if (sure || (equal && eq_mine < take)) {
-            const int32_t pos = at_out + sures + __popc(se & lt) + min(eq_mine, take) - min(eq_before, take);
-            if (pos < n_select) out[pos] = p0 + i;
-        }
-        at_out += sures_all + min(eq_before + eq_all, take) - min(eq_before, take);
-        eq_before += eq_all;
         __syncthreads();
+        uint32_t in = tid * 32 < here ? sh.in_mask[tid] : 0;
+        if (ties) {  // of the equal ones the first
+            uint32_t eq = tid * 32 < here ? sh.eq_mask[tid] : 0;
+            const int2 before = sum_before(__popc(eq), sh.ired);
+            for (int32_t i = before.x; eq && i < left; ++i) in |= eq & -eq, eq &= eq - 1;
+            left -= min(left, before.y);
+        }
+        const int2 before = sum_before(__popc(in), sh.ired);
+        int32_t pos = at_out + before.x;
+        at_out += before.y;
+        for (; in; in &= in - 1, ++pos)
+            if (pos < n_select) out[pos] = first + tid * 32 + __ffs(in) - 1;
+        __syncthreads();
+    }
+    // Fewer than wanted only where pages out of range were not ranked.
+    for (int32_t i = at_out + tid; i < n_select; i += kThreads) out[i] = -1;
+}
+
+// A float32 score's error over the sum of its terms' sizes: the coefficients' sums (G - 1), products (1), at most 8 terms
+// in a lane's sum and 5 sums of lanes (13), each rounding 2^-24 of something no larger; the sizes' own sums as much.
+__device__ __forceinline__ float error_of(const PagedMeta& m) { return (32 + 2 * m.group) * 0x1p-24f; }
+
+// One block per (sequence, kv head).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) pick_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
+                                                        const T* __restrict__ bounds, const int32_t* __restrict__ table,
+                                                        const int32_t* __restrict__ seq_len, int32_t n_select,
+                                                        int32_t keep_first, int32_t keep_last, uint2* scores,
+                                                        int32_t* __restrict__ pages, int32_t* status) {
+    extern __shared__ uint32_t copy[];
+    __shared__ __align__(16) Shared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x, b = row / m.hkv, g = row % m.hkv;
+    if (__syncthreads_or(status_bad(status))) return;
+    const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
+    const int32_t* trow = table + b * m.table_stride;
+    int32_t* out = pages + (int64_t)row * n_select;
+    if (!r.scored) {
+        for (int i = tid; i < n_select; i += kThreads)
+            out[i] = i >= r.want ? -1 : r.count <= n_select || i < r.lead ? i : r.tail + i - r.lead;
+        for (int i = tid; i < r.count; i += kThreads) paged_page(m, trow, i, status);  // checked all the same
+        return;
+    }
+    scores += (int64_t)row * m.max_pages;
+    Keys<uint32_t> keys{copy, r.count, 1};
+    if (r.count > kInShared) keys = {reinterpret_cast<uint32_t*>(scores), r.count, 2};
+    uint64_t lo = ~0ull, hi = 0;
+    float size = 0.f;
+#pragma unroll 4
+    for (int32_t p = tid; p < r.count; p += kThreads) {
+        const uint2 x = scores[p];
+        if (keys.step == 1) copy[p] = x.x;
+        if (x.x) lo = min(lo, (uint64_t)x.x), hi = max(hi, (uint64_t)x.x);
+        size = max_nan(size, __uint_as_float(x.y));
+    }
+#pragma unroll
+    for (int i = 0; i < kBins / kThreads; ++i) sh.hist[i * kThreads + tid] = 0;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) size = max_nan(size, __shfl_xor_sync(0xffffffffu, size, x));
+    if (lane == 0) sh.ired[warp] = __float_as_int(size);
+    range_of(sh, lo, hi);
+    size = __int_as_float(sh.ired[lane % kWarps]);
+#pragma unroll
+    for (int x = kWarps / 2; x; x >>= 1) size = max_nan(size, __shfl_xor_sync(0xffffffffu, size, x));
+    const float err = fmaf(size, 2.f * error_of(m), 0x1p-140f);  // twice the error (and what denormal terms may lose)
+
+    // The bin with the n-th largest; pages from 2 errors below it to 2 above cannot be told from the n-th largest.
+    const int32_t open = r.want - (r.lead + r.count - r.tail);
+    int32_t need = open, in_bin;
+    narrow(keys, sh, lo, hi, need, in_bin);
+    uint64_t from = 1, to = ~0u;
+    if (in_bin && err < INFINITY) {
+        from = max(score_key(__fsub_rd(key_score((uint32_t)lo), err)), 1u);
+        to = score_key(__fadd_ru(key_score((uint32_t)hi), err));
+    }
+    const int32_t near = gather(keys, sh, from, to);
+    int32_t sure = 0;
+    keys.each([&](int32_t, uint32_t k) { sure += k > to; });
+    need = open - sum_before(sure, sh.ired).y;
+    if (near <= need) {
+        write_pages(keys, sh, r, from, 1, 0, 0, out, n_select);
+        return;
+    }
+    const T* qg = q + b * q_stride + (int64_t)g * m.group * m.d;
+    const T* head = bounds + (int64_t)g * 2 * m.d;
+    if (near <= kCands && to < ~0u) {
+        for (int i = warp; i < near; i += kWarps) {
+            const uint64_t k = exact<T>(m, qg, head, trow, sh.cand_page[i], status);
+            if (lane == 0) sh.cand_key[i] = k;
+        }
+        __syncthreads();
+        if (tid < near) keys.at[(int64_t)sh.cand_page[tid] * keys.step] = place(sh, near) < need ? ~0u : 0;
+        __syncthreads();
+        write_pages(keys, sh, r, to + 1, 1, 0, 0, out, n_select);
+        return;
+    }
+    // Too many: all their scores in float64, in the place of the float32 ones; surely taken ones ~0.
+    Keys<uint64_t> wide{reinterpret_cast<uint64_t*>(scores), r.count, 1};
+    lo = ~0ull, hi = 0;
+    for (int32_t p = warp; p < r.count; p += kWarps) {
+        const uint32_t k = scores[p].x;
+        const uint64_t x = k > to ? ~0ull : k >= from ? exact<T>(m, qg, head, trow, p, status) : 0;
+        __syncwarp();
+        if (lane == 0) wide.at[p] = x;
+        if (x && ~x) lo = min(lo, x), hi = max(hi, x);
+    }
+    range_of(sh, lo, hi);
+    narrow(wide, sh, lo, hi, need, in_bin);
+    if (in_bin <= need) {
+        write_pages(wide, sh, r, lo, 1, 0, 0, out, n_select);
+    } else if (in_bin <= kCands) {
+        gather(wide, sh, lo, hi);
+        if (tid < in_bin) wide.at[sh.cand_page[tid]] = place(sh, in_bin) < need ? ~0ull : 0;
+        __syncthreads();
+        write_pages(wide, sh, r, hi + 1, 1, 0, 0, out, n_select);
+    } else {
+        write_pages(wide, sh, r, hi + 1, lo, hi, need, out, n_select);
     }
 }
 
 template <typename T, int LP, int NC>
 cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_bounds, const int32_t* table,
                    const int32_t* seq_len, int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t* pages,
-                   int32_t* status, cudaStream_t st) {
+                   int32_t* status, void* ws, cudaStream_t st) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    // Blocks a row: as many as its scores need room for, then until the blocks fill the GPU twice, while each keeps
-    // 128 pages.
-    const int64_t rows = (int64_t)m.n_seqs * m.hkv;
-    int cl = 1;
-    while (cl < kMaxCluster && (m.max_pages > (int64_t)cl * kMaxShare ||
-                                (rows * cl < 2 * sms && m.max_pages > (int64_t)cl * 2 * 128)))
-        cl *= 2;
-    auto kern = select_kernel<T, LP, NC>;
-    const size_t smem = sizeof(uint64_t) * ((m.max_pages + cl - 1) / cl);
+    auto pick = pick_kernel<T>;
     static SmemGrants granted;
-    e = allow_smem((const void*)kern, sizeof(uint64_t) * kMaxShare, granted);
+    e = allow_smem((const void*)pick, sizeof(uint32_t) * kInShared, granted);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(rows * cl));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cl;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return note_error(cudaLaunchKernelEx(&cfg, kern, m, (const T*)q, q_stride, (const T*)k_bounds, table, seq_len,
-                                         n_select, keep_first, keep_last, pages, status, (int32_t)cl),
-                      "paged select");
+    const size_t lens = sizeof(int32_t) * std::max(m.n_seqs + 1, kWarps * 36);
+    score_kernel<T, LP, NC><<<sms, kThreads, lens, st>>>(m, (const T*)q, q_stride, (const T*)k_bounds, table, seq_len,
+                                                         n_select, keep_first, keep_last, (uint2*)ws, status);
+    pick<<<m.n_seqs * m.hkv, kThreads, sizeof(uint32_t) * std::min(m.max_pages, kInShared), st>>>(
+        m, (const T*)q, q_stride, (const T*)k_bounds, table, seq_len, n_select, keep_first, keep_last, (uint2*)ws, pages,
+        status);
+    return note_error(cudaGetLastError(), "paged select");
 }
 
 }  // namespace
 
+size_t paged_select_workspace(const PagedMeta& m) { return sizeof(uint2) * m.n_seqs * m.hkv * m.max_pages; }
+
 cudaError_t launch_paged_select(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_bounds,
                                 const int32_t* table, const int32_t* seq_len, int32_t n_select, int32_t keep_first,
-                                int32_t keep_last, int32_t* pages, int32_t* status, cudaStream_t st) {
+                                int32_t keep_last, int32_t* pages, int32_t* status, void* ws, cudaStream_t st) {
 #define SPLITKV_SELECT(T, LP, NC) \
-    launch<T, LP, NC>(m, q, q_stride, k_bounds, table, seq_len, n_select, keep_first, keep_last, pages, status, st)
+    launch<T, LP, NC>(m, q, q_stride, k_bounds, table, seq_len, n_select, keep_first, keep_last, pages, status, ws, st)
     const int chunks = 2 * m.d * (m.dtype == SPLITKV_BF16 ? 2 : 4) / 16;  // 16-byte pieces of a page's bounds
     if (m.dtype == SPLITKV_BF16) {
         if (chunks <= 8) return SPLITKV_SELECT(__nv_bfloat16, 8, 1);

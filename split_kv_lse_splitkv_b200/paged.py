@@ -206,9 +206,11 @@ class PagedKV:
             return self._on(self.select, stream, q, page_table, seq_lens, n_select, keep_first, keep_last, pages)
         if pages is None:
             pages = seq_lens.new_empty(shape)
-        # No sequence has more pages than its row: any larger number says the same.
+        # Scratch of the call alone: 8 bytes per page and kv head. No sequence has more pages than its row: any larger
+        # number of kept ones says the same.
+        ws = seq_lens.new_empty((n * self.n_kv_heads * page_table.shape[1] * 2 + 4,))
         B.splitkv_paged_select(layout, n, q, qs, self.k_bounds, page_table, seq_lens, n_select,
-                               min(int(keep_first), _MOST), min(int(keep_last), _MOST), pages, self.status,
+                               min(int(keep_first), _MOST), min(int(keep_last), _MOST), pages, self.status, ws,
                                _raw_stream(self._index))
         return pages
 

@@ -177,8 +177,11 @@ def test_append_refusals():
 def test_select_refusals():
     f = torch.empty(1 << 16, dtype=torch.int32)
     good = dict(n_seqs=4, q=f, q_stride=512, k_bounds=f, page_table=f, seq_len=f, n_select=3, keep_first=1, keep_last=1,
-                pages=f, status=f)
-    for kw, code in ((dict(q=None), B.EINVAL), (dict(k_bounds=None), B.EINVAL), (dict(page_table=None), B.EINVAL),
+                pages=f, status=f, workspace=f)
+    assert B.splitkv_paged_select_workspace_size(desc(), 4) == 4 * 2 * 4 * 8
+    assert B.splitkv_paged_select_workspace_size(desc(max_pages=B.PAGED_MAX_SELECT_PAGES + 1), 4) == 0
+    for kw, code in ((dict(workspace=None), B.ENOSPACE), (dict(workspace=f[:63]), B.ENOSPACE),
+                     (dict(workspace=f[1:]), B.EINVAL), (dict(q=None), B.EINVAL), (dict(k_bounds=None), B.EINVAL), (dict(page_table=None), B.EINVAL),
                      (dict(seq_len=None), B.EINVAL), (dict(pages=None), B.EINVAL), (dict(status=None), B.EINVAL),
                      (dict(n_select=0), B.EINVAL), (dict(keep_first=-1), B.EINVAL), (dict(keep_last=-1), B.EINVAL),
                      (dict(k_bounds=f[2:]), B.EINVAL), (dict(n_select=B.PAGED_MAX_SELECT_PAGES + 1), B.EUNSUPPORTED)):
