@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
     __shared__ int32_t n_tokens, last_pos;
     __shared__ uint4 red[kWarps][32][4];      // minima and maxima of a lane's two pieces
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    after_previous();
     if (__syncthreads_or(status_bad(status))) return;
 
     if (blockIdx.x >= kv_blocks) {
@@ -438,8 +439,9 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     const int turned = a.rope_dim / 2 / Vec<T>::kN, rows = 32 / (turned + ((m.d - a.rope_dim) / Vec<T>::kN + 1) / 2);
     int32_t heads = std::min(m.hq, a.n_tokens * m.hq / rows < kSms * 32 ? rows : 4 * rows);
     const int64_t q_blocks = a.q ? (a.n_tokens * ((m.hq + heads - 1) / heads) + kWarps - 1) / kWarps : 0;
-    append_kernel<T><<<(unsigned)(kv_blocks + q_blocks), kThreads, 0, st>>>(m, a, status, kv_blocks, slice, heads);
-    return note_error(cudaGetLastError(), "paged append");
+    return note_error(launch_overlapped(append_kernel<T>, kv_blocks + q_blocks, kThreads, 0, st, m, a, status, kv_blocks,
+                                        slice, heads),
+                      "paged append");
 }
 
 }  // namespace

@@ -424,8 +424,10 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row_groups = (m.group + R - 1) / R;
 
+    after_previous();
+
     // ---- the line of units
-    const bool skip = __any_sync(0xffffffffu, status_bad(status));
+    const bool bad = status_bad(status);
     auto units_of = [&](int b) {
         const int32_t len = paged_len(m, seq_len, b, status);
         int32_t n = len;
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         }
         __syncthreads();
     }
+    const bool skip = __any_sync(0xffffffffu, bad);
     Line L{prefix, m.n_seqs, m.hkv * row_groups, 0, 0};
     L.total = (int64_t)prefix[m.n_seqs] * L.per_seq;
     L.per_part = max(div_units(L.total + gridDim.x - 1, gridDim.x), (int64_t)W);
@@ -821,9 +824,10 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     e = allow_smem((const void*)kern, sizeof(P) * W * 2 + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), granted);
     if (e != cudaSuccess) return e;
     const int grid = std::min(sms, kMaxParts);
-    kern<<<grid, W * 32, smem, st>>>(m, (const T*)q, q_stride, (const T*)k_cache, (const T*)v_cache, table, seq_len,
-                                     pages, n_select, (T*)o, lse, status, (uint32_t*)ws, (char*)ws + kCounterBytes);
-    return note_error(cudaGetLastError(), "paged decode");
+    return note_error(launch_overlapped(kern, grid, W * 32, smem, st, m, (const T*)q, q_stride, (const T*)k_cache,
+                                        (const T*)v_cache, table, seq_len, pages, n_select, (T*)o, lse, status,
+                                        (uint32_t*)ws, (char*)ws + kCounterBytes),
+                      "paged decode");
 }
 
 }  // namespace

@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
     extern __shared__ int32_t prefix_all[];  // pages to score of the sequences before b
     int32_t* prefix = prefix_all;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (__any_sync(0xffffffffu, status_bad(status)) && m.n_seqs <= 32) return;
+    after_previous();
+    const bool bad = status_bad(status);
     auto pages_of = [&](int b) {
         const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
         return r.scored ? r.count : 0;
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
         }
         __syncthreads();
     }
+    if (__any_sync(0xffffffffu, bad)) return;
     const int64_t total = (int64_t)prefix[m.n_seqs] * m.hkv;
     const int32_t n_warps = gridDim.x * kWarps, me = warp * gridDim.x + blockIdx.x;  // neighbours on other SMs
     const int64_t per = max((total + n_warps - 1) / n_warps, (int64_t)kStep);
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
         }
         const int32_t count = prefix[b + 1] - prefix[b];
         const int64_t rem = u - (int64_t)prefix[b] * m.hkv;
-        const int32_t g = (int32_t)(rem / count);
+        const int32_t g = rem >> 32 ? (int32_t)(rem / count) : (int32_t)((uint32_t)rem / (uint32_t)count);
         int32_t p = (int32_t)(rem - (int64_t)g * count);
         const int32_t p_end = (int32_t)min((int64_t)count, p + (u_end - u));
         u += p_end - p;
@@ -191,9 +193,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
             }
         uint4 x[kV][NC], ahead[kV][NC];
         load(mine, x);
-        for (;;) {
-            const int32_t after = entry(p + 2 * kStep);
-            load(next, ahead);
+        auto round = [&](const uint4 (&x)[kV][NC]) {
             float s[kV], size = 0.f;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
@@ -228,19 +228,26 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
                     s[0] += __shfl_xor_sync(0xffffffffu, s[0], step);
                 }
             }
-            const int v = sub / (LP / kV), mine_at = v * kPer + at;
-            const int32_t page = __shfl_sync(0xffffffffu, mine, mine_at & 31);
-            if (sub % (LP / kV) == 0 && p + mine_at < p_end) {
-                const int32_t at_p = p + mine_at;
+            const int v = sub / (LP / kV), at_p = p + v * kPer + at;
+            const int32_t page = __shfl_sync(0xffffffffu, mine, (v * kPer + at) & 31);
+            if (sub % (LP / kV) == 0 && at_p < p_end) {
                 const bool kept = at_p < keep_first || at_p >= count - keep_last;
                 out[at_p] = make_uint2(kept || page < 0 ? 0 : score_key(s[0]), __float_as_uint(size));
             }
-            if ((p += kStep) >= p_end) break;
-            mine = next, next = after;
-#pragma unroll
-            for (int v = 0; v < kV; ++v)
-#pragma unroll
-                for (int k = 0; k < NC; ++k) x[v][k] = ahead[v][k];
+            mine = next;
+            p += kStep;
+        };
+        for (;;) {
+            int32_t after = entry(p + 2 * kStep);
+            load(next, ahead);
+            round(x);
+            next = after;
+            if (p >= p_end) break;
+            after = entry(p + 2 * kStep);
+            load(next, x);
+            round(ahead);
+            next = after;
+            if (p >= p_end) break;
         }
     }
 }
@@ -253,11 +260,11 @@ struct Shared {
     int32_t cand_page[kCands];
     uint64_t red[2 * kWarps];
     int32_t ired[kWarps];
-    int32_t found[4];
+    int32_t found[6];
     uint32_t in_mask[kWords], eq_mask[kWords];
 };
 
-// Sum of x over the threads before this one; `all`: over every thread. Two barriers.
+// Sum of x over the threads before this one, and over all of them. Two barriers.
 __device__ __noinline__ int2 sum_before(int32_t x, int32_t* warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t incl = x;
@@ -290,11 +297,12 @@ struct Keys {
 // from the bin's top. Ends with at most kCands keys in the bin, or with all of them needed, or all equal. hist is zero
 // before and after.
 template <typename K>
-__device__ __noinline__ void narrow(const Keys<K>& keys, Shared& sh, uint64_t& lo, uint64_t& hi, int32_t& need,
-                                    int32_t& in_bin) {
+__device__ __forceinline__ void narrow(const Keys<K>& keys, Shared& sh, K& lo, K& hi, int32_t& need, int32_t& in_bin) {
     const int tid = threadIdx.x;
-    const uint64_t range = hi - lo;
-    int shift = lo < hi && range >> kBits ? 64 - kBits - __clzll((long long)range) : 0;
+    const K range = hi - lo;
+    int shift = 0;
+    if (lo < hi && range >> kBits)
+        shift = 8 * (int)sizeof(K) - kBits - (sizeof(K) == 8 ? __clzll((long long)range) : __clz((int)range));
     for (;;) {
         if (tid < 4) sh.found[tid] = 0;
         __syncthreads();
@@ -313,55 +321,40 @@ __device__ __noinline__ void narrow(const Keys<K>& keys, Shared& sh, uint64_t& l
         int32_t above = sum_before(sum, sh.ired).x;
         if (above < need && above + sum >= need) {
             int k = 0;
-            while (above + (int32_t)v[k] < need) above += v[k++];
+#pragma unroll
+            for (int i = 0; i < kEach - 1; ++i)
+                if (k == i && above + (int32_t)v[i] < need) above += v[i], ++k;
             sh.found[0] = kBins - 1 - kEach * tid - k;
             sh.found[1] = above;
-            sh.found[2] = v[k];
+            sh.found[2] = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
         }
         __syncthreads();
         need -= sh.found[1];
         in_bin = sh.found[2];
-        lo += (uint64_t)sh.found[0] << shift;
-        const uint64_t width = (1ull << shift) - 1;
+        lo += (K)sh.found[0] << shift;
+        const K width = ((K)1 << shift) - 1;
         if (hi - lo > width) hi = lo + width;  // (the last bin may reach past the range)
-        __syncthreads();
         if (in_bin <= kCands || in_bin <= need || shift == 0) return;
         shift = max(0, shift - kBits);
+        __syncthreads();
     }
 }
 
-// Smallest and largest of the threads' values.
-__device__ __noinline__ void range_of(Shared& sh, uint64_t& lo, uint64_t& hi) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 1
-    for (int x = 16; x; x >>= 1) {
-        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
-        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, x));
-    }
-    if (lane == 0) sh.red[warp] = lo, sh.red[kWarps + warp] = hi;
-    __syncthreads();
-    lo = sh.red[lane % kWarps], hi = sh.red[kWarps + lane % kWarps];
-#pragma unroll 1
-    for (int x = kWarps / 2; x; x >>= 1) {
-        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
-        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, x));
-    }
-    __syncthreads();
-}
-
-// The keys in [from, to] into the list of candidates; how many there are (those past kCands are only counted).
+// The keys in [from, to] into the list of candidates. Their number (those past kCands are only counted), and how many of
+// them are above `mark`.
 template <typename K>
-__device__ __noinline__ int32_t gather(const Keys<K>& keys, Shared& sh, uint64_t from, uint64_t to) {
-    if (threadIdx.x == 0) sh.found[3] = 0;
+__device__ __forceinline__ int2 gather(const Keys<K>& keys, Shared& sh, K from, K to, K mark) {
+    if (threadIdx.x < 2) sh.found[4 + threadIdx.x] = 0;
     __syncthreads();
     keys.each([&](int32_t p, K k) {
         if (k >= from && k <= to) {
-            const int32_t i = atomicAdd(&sh.found[3], 1);
+            const int32_t i = atomicAdd(&sh.found[4], 1);
+            if (k > mark) atomicAdd(&sh.found[5], 1);
             if (i < kCands) sh.cand_key[i] = k, sh.cand_page[i] = p;
         }
     });
     __syncthreads();
-    return sh.found[3];
+    return make_int2(sh.found[4], sh.found[5]);
 }
 
 // How many of the n candidates come before this thread's: larger keys, equal keys of lower pages.
@@ -373,6 +366,16 @@ __device__ __forceinline__ int32_t place(const Shared& sh, int32_t n) {
     return better;
 }
 
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4]) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    f[0] = __uint_as_float(x.x << 16), f[1] = __uint_as_float(x.x & 0xffff0000u);
+    f[2] = __uint_as_float(x.y << 16), f[3] = __uint_as_float(x.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+}
+
 // The key of page p's float64 score, on one warp: the group's query channels again, in float64.
 template <typename T>
 __device__ __noinline__ uint64_t exact(const PagedMeta& m, const T* q, const T* head, const int32_t* trow, int32_t p,
@@ -382,15 +385,29 @@ __device__ __noinline__ uint64_t exact(const PagedMeta& m, const T* q, const T* 
     if (page < 0) return 0;
     const T* x = head + page * ((int64_t)m.hkv * 2 * m.d);
     double s = 0.0;
-    for (int i = lane; i < m.d; i += 32) {
-        double up = 0.0, down = 0.0;
-        for (int h = 0; h < m.group; ++h) {
-            const double y = to_f32<T>(q[(int64_t)h * m.d + i]);
-            up += y >= 0.0 ? y : y != y ? y : 0.0;
-            down += y <= 0.0 ? y : y != y ? y : 0.0;
+    const int i = 4 * lane;  // d is a multiple of 4, at most 128: all loads at once
+    if (i < m.d) {
+        double up[4] = {}, down[4] = {};
+        float lo[4], hi[4];
+        load4(x + i, lo);
+        load4(x + m.d + i, hi);
+        for (int h0 = 0; h0 < m.group; h0 += 8) {
+            float y[8][4];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                if (h0 + h < m.group) load4(q + (int64_t)(h0 + h) * m.d + i, y[h]);
+                else y[h][0] = y[h][1] = y[h][2] = y[h][3] = 0.f;
+            }
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    up[j] += y[h][j] > 0.f ? y[h][j] : 0.f;
+                    down[j] += y[h][j] > 0.f ? 0.f : y[h][j];
+                }
         }
-        s = fma((double)to_f32<T>(x[i]), down, s);
-        s = fma((double)to_f32<T>(x[m.d + i]), up, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fma((double)lo[j], down[j], s), s = fma((double)hi[j], up[j], s);
     }
 #pragma unroll
     for (int y = 16; y; y >>= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
@@ -399,19 +416,23 @@ __device__ __noinline__ uint64_t exact(const PagedMeta& m, const T* q, const T* 
 
 // Writes the pages taken, in order: the kept ones, those with keys >= take, and of those in [lo, hi] the first `ties`.
 template <typename K>
-__device__ __noinline__ void write_pages(const Keys<K>& keys, Shared& sh, const Row& r, uint64_t take, uint64_t lo,
-                                         uint64_t hi, int32_t ties, int32_t* out, int32_t n_select) {
+__device__ __noinline__ void write_pages(const Keys<K>& keys, Shared& sh, const Row& r, K take, K lo, K hi,
+                                         int32_t ties, int32_t* out, int32_t n_select) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t at_out = 0, left = ties;
     for (int32_t first = 0; first < r.count; first += kSpan) {
         const int32_t here = min(r.count - first, kSpan);
+#pragma unroll 4
         for (int32_t i = warp * 32; i < here; i += kThreads) {
             const int32_t p = first + i + lane;
-            const uint64_t key = p < r.count ? keys.at[(int64_t)p * keys.step] : 0;
+            const K key = p < r.count ? keys.at[(int64_t)p * keys.step] : 0;
             const bool kept = p < r.count && (p < r.lead || p >= r.tail);
             const uint32_t in = __ballot_sync(0xffffffffu, kept || (key && key >= take));
-            const uint32_t eq = __ballot_sync(0xffffffffu, ties && key >= lo && key <= hi);
-            if (lane == 0) sh.in_mask[i / 32] = in, sh.eq_mask[i / 32] = eq;
+            if (ties) {
+                const uint32_t eq = __ballot_sync(0xffffffffu, key >= lo && key <= hi);
+                if (lane == 0) sh.eq_mask[i / 32] = eq;
+            }
+            if (lane == 0) sh.in_mask[i / 32] = in;
         }
         __syncthreads();
         uint32_t in = tid * 32 < here ? sh.in_mask[tid] : 0;
@@ -426,10 +447,45 @@ __device__ __noinline__ void write_pages(const Keys<K>& keys, Shared& sh, const 
         at_out += before.y;
         for (; in; in &= in - 1, ++pos)
             if (pos < n_select) out[pos] = first + tid * 32 + __ffs(in) - 1;
-        __syncthreads();
     }
     // Fewer than wanted only where pages out of range were not ranked.
     for (int32_t i = at_out + tid; i < n_select; i += kThreads) out[i] = -1;
+}
+
+// More pages than are ranked one by one cannot be told from the n-th largest: the scores of all of them in float64, in the
+// place of the float32 ones, and those that are sure to be taken ~0. Rare (equal pages, scores that are not finite).
+template <typename T>
+__device__ __noinline__ void pick_wide(const PagedMeta& m, const T* q, const T* head, const int32_t* trow, uint2* scores,
+                                       Shared& sh, const Row& r, uint32_t from, uint32_t to, int32_t need, int32_t* out,
+                                       int32_t n_select, int32_t* status) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Keys<uint64_t> wide{reinterpret_cast<uint64_t*>(scores), r.count, 1};
+    uint64_t lo = ~0ull, hi = 0;
+    for (int32_t p = warp; p < r.count; p += kWarps) {
+        const uint32_t k = scores[p].x;
+        const uint64_t x = k > to ? ~0ull : k >= from ? exact<T>(m, q, head, trow, p, status) : 0;
+        __syncwarp();
+        if (lane == 0) wide.at[p] = x;
+        if (x && ~x) lo = min(lo, x), hi = max(hi, x);
+    }
+    if (lane == 0) sh.red[warp] = lo, sh.red[kWarps + warp] = hi;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) lo = min(lo, sh.red[w]), hi = max(hi, sh.red[kWarps + w]);
+    int32_t in_bin;
+    narrow(wide, sh, lo, hi, need, in_bin);
+    int32_t ties = 0;
+    uint64_t take = lo;
+    if (in_bin > need) {
+        take = hi + 1;
+        if (in_bin <= kCands) {
+            gather(wide, sh, lo, hi, hi);
+            if (threadIdx.x < in_bin) wide.at[sh.cand_page[threadIdx.x]] = place(sh, in_bin) < need ? ~0ull : 0;
+        } else {
+            ties = need;
+        }
+        __syncthreads();
+    }
+    write_pages(wide, sh, r, take, lo, hi, ties, out, n_select);
 }
 
 // A float32 score's error over the sum of its terms' sizes: the coefficients' sums (G - 1), products (1), at most 8 terms
@@ -447,91 +503,95 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(PagedMeta m, const T* __
     __shared__ __align__(16) Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x, b = row / m.hkv, g = row % m.hkv;
-    if (__syncthreads_or(status_bad(status))) return;
+    scores += (int64_t)row * m.max_pages;
+    after_previous();
+    // The first scores are asked for before the length is known (a row has max_pages places, written or not).
+    constexpr int kAhead = 8;
+    uint2 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = i * kThreads + tid < m.max_pages ? scores[i * kThreads + tid] : make_uint2(0, 0);
+    const bool bad = status_bad(status);
     const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
     const int32_t* trow = table + b * m.table_stride;
     int32_t* out = pages + (int64_t)row * n_select;
+    reinterpret_cast<uint4*>(sh.hist)[tid] = make_uint4(0, 0, 0, 0);
+    if (__syncthreads_or(bad)) return;
     if (!r.scored) {
         for (int i = tid; i < n_select; i += kThreads)
             out[i] = i >= r.want ? -1 : r.count <= n_select || i < r.lead ? i : r.tail + i - r.lead;
         for (int i = tid; i < r.count; i += kThreads) paged_page(m, trow, i, status);  // checked all the same
         return;
     }
-    scores += (int64_t)row * m.max_pages;
     Keys<uint32_t> keys{copy, r.count, 1};
     if (r.count > kInShared) keys = {reinterpret_cast<uint32_t*>(scores), r.count, 2};
-    uint64_t lo = ~0ull, hi = 0;
+    uint32_t lo = ~0u, hi = 0;
     float size = 0.f;
-#pragma unroll 4
-    for (int32_t p = tid; p < r.count; p += kThreads) {
-        const uint2 x = scores[p];
+    auto see = [&](int32_t p, const uint2& x) {
         if (keys.step == 1) copy[p] = x.x;
-        if (x.x) lo = min(lo, (uint64_t)x.x), hi = max(hi, (uint64_t)x.x);
+        lo = min(lo, x.x - 1), hi = max(hi, x.x);  // (0, not ranked, is the largest there)
         size = max_nan(size, __uint_as_float(x.y));
-    }
+    };
 #pragma unroll
-    for (int i = 0; i < kBins / kThreads; ++i) sh.hist[i * kThreads + tid] = 0;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) size = max_nan(size, __shfl_xor_sync(0xffffffffu, size, x));
-    if (lane == 0) sh.ired[warp] = __float_as_int(size);
-    range_of(sh, lo, hi);
-    size = __int_as_float(sh.ired[lane % kWarps]);
-#pragma unroll
-    for (int x = kWarps / 2; x; x >>= 1) size = max_nan(size, __shfl_xor_sync(0xffffffffu, size, x));
+    for (int i = 0; i < kAhead; ++i)
+        if (i * kThreads + tid < r.count) see(i * kThreads + tid, x[i]);
+    for (int32_t p = kAhead * kThreads + tid; p < r.count; p += kThreads) see(p, scores[p]);
+    // Sizes are not negative: as integers they have the floats' order, NaN on top.
+    static_assert(kWarps == 16, "two values a lane");
+    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size) & 0x7fffffffu);
+    if (lane == 0) sh.red[warp] = (uint64_t)hi << 32 | lo, sh.ired[warp] = (int32_t)most;
+    __syncthreads();
+    const uint64_t both = sh.red[lane % kWarps];
+    lo = __reduce_min_sync(0xffffffffu, (uint32_t)both) + 1, hi = __reduce_max_sync(0xffffffffu, (uint32_t)(both >> 32));
+    size = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)sh.ired[lane % kWarps]));
     const float err = fmaf(size, 2.f * error_of(m), 0x1p-140f);  // twice the error (and what denormal terms may lose)
+    if (lo == 0) lo = ~0u, hi = 0;                               // nothing ranked
 
     // The bin with the n-th largest; pages from 2 errors below it to 2 above cannot be told from the n-th largest.
     const int32_t open = r.want - (r.lead + r.count - r.tail);
     int32_t need = open, in_bin;
     narrow(keys, sh, lo, hi, need, in_bin);
-    uint64_t from = 1, to = ~0u;
-    if (in_bin && err < INFINITY) {
-        from = max(score_key(__fsub_rd(key_score((uint32_t)lo), err)), 1u);
-        to = score_key(__fadd_ru(key_score((uint32_t)hi), err));
+    uint32_t from = 1, to = ~0u;
+    const bool finite = in_bin && err < INFINITY;
+    if (finite) {
+        from = max(score_key(__fsub_rd(key_score(lo), err)), 1u);
+        to = score_key(__fadd_ru(key_score(hi), err));
     }
-    const int32_t near = gather(keys, sh, from, to);
-    int32_t sure = 0;
-    keys.each([&](int32_t, uint32_t k) { sure += k > to; });
-    need = open - sum_before(sure, sh.ired).y;
-    if (near <= need) {
-        write_pages(keys, sh, r, from, 1, 0, 0, out, n_select);
-        return;
-    }
-    const T* qg = q + b * q_stride + (int64_t)g * m.group * m.d;
-    const T* head = bounds + (int64_t)g * 2 * m.d;
-    if (near <= kCands && to < ~0u) {
-        for (int i = warp; i < near; i += kWarps) {
-            const uint64_t k = exact<T>(m, qg, head, trow, sh.cand_page[i], status);
-            if (lane == 0) sh.cand_key[i] = k;
+    const int2 near = gather(keys, sh, from, to, hi);
+    // Above them: what narrow() counted above the bin, without those that are near.
+    need = finite ? need + near.y : in_bin ? open : near.x;
+    uint32_t take = from;
+    if (near.x > need) {
+        const T* qg = q + b * q_stride + (int64_t)g * m.group * m.d;
+        const T* head = bounds + (int64_t)g * 2 * m.d;
+        if (near.x > kCands || !finite) {
+            pick_wide<T>(m, qg, head, trow, scores, sh, r, from, to, need, out, n_select, status);
+            return;
         }
+        // The n-th largest itself; usually no other page is within 2 errors of it.
+        const uint32_t mine = tid < near.x ? (uint32_t)sh.cand_key[tid] : 0;
+        const int32_t before = tid < near.x ? place(sh, near.x) : INT32_MAX;
+        if (before == need - 1) sh.found[0] = (int32_t)mine;
         __syncthreads();
-        if (tid < near) keys.at[(int64_t)sh.cand_page[tid] * keys.step] = place(sh, near) < need ? ~0u : 0;
+        const float nth = key_score((uint32_t)sh.found[0]);
+        const uint32_t below = score_key(__fsub_rd(nth, err)), above = score_key(__fadd_ru(nth, err));
+        const int32_t sure = __syncthreads_count(mine > above), open2 = __syncthreads_count(mine && mine >= below) - sure;
+        bool in = mine && mine >= below;
+        if (sure + open2 > need) {  // the others in float64; those above come first, those below last
+            for (int i = warp; i < near.x; i += kWarps) {
+                const uint32_t k = (uint32_t)sh.cand_key[i];
+                const uint64_t e = k > above ? ~0ull : k < below ? 0 : exact<T>(m, qg, head, trow, sh.cand_page[i], status);
+                __syncwarp();
+                if (lane == 0) sh.cand_key[i] = e;
+            }
+            __syncthreads();
+            in = tid < near.x && place(sh, near.x) < need;
+        }
+        if (tid < near.x) keys.at[(int64_t)sh.cand_page[tid] * keys.step] = in ? ~0u : 0;
+        take = to + 1;
         __syncthreads();
-        write_pages(keys, sh, r, to + 1, 1, 0, 0, out, n_select);
-        return;
     }
-    // Too many: all their scores in float64, in the place of the float32 ones; surely taken ones ~0.
-    Keys<uint64_t> wide{reinterpret_cast<uint64_t*>(scores), r.count, 1};
-    lo = ~0ull, hi = 0;
-    for (int32_t p = warp; p < r.count; p += kWarps) {
-        const uint32_t k = scores[p].x;
-        const uint64_t x = k > to ? ~0ull : k >= from ? exact<T>(m, qg, head, trow, p, status) : 0;
-        __syncwarp();
-        if (lane == 0) wide.at[p] = x;
-        if (x && ~x) lo = min(lo, x), hi = max(hi, x);
-    }
-    range_of(sh, lo, hi);
-    narrow(wide, sh, lo, hi, need, in_bin);
-    if (in_bin <= need) {
-        write_pages(wide, sh, r, lo, 1, 0, 0, out, n_select);
-    } else if (in_bin <= kCands) {
-        gather(wide, sh, lo, hi);
-        if (tid < in_bin) wide.at[sh.cand_page[tid]] = place(sh, in_bin) < need ? ~0ull : 0;
-        __syncthreads();
-        write_pages(wide, sh, r, hi + 1, 1, 0, 0, out, n_select);
-    } else {
-        write_pages(wide, sh, r, hi + 1, lo, hi, need, out, n_select);
-    }
+    write_pages(keys, sh, r, take, 1u, 0u, 0, out, n_select);
 }
 
 template <typename T, int LP, int NC>
@@ -546,12 +606,13 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     e = allow_smem((const void*)pick, sizeof(uint32_t) * kInShared, granted);
     if (e != cudaSuccess) return e;
     const size_t lens = sizeof(int32_t) * std::max(m.n_seqs + 1, kWarps * 36);
-    score_kernel<T, LP, NC><<<sms, kThreads, lens, st>>>(m, (const T*)q, q_stride, (const T*)k_bounds, table, seq_len,
-                                                         n_select, keep_first, keep_last, (uint2*)ws, status);
-    pick<<<m.n_seqs * m.hkv, kThreads, sizeof(uint32_t) * std::min(m.max_pages, kInShared), st>>>(
-        m, (const T*)q, q_stride, (const T*)k_bounds, table, seq_len, n_select, keep_first, keep_last, (uint2*)ws, pages,
-        status);
-    return note_error(cudaGetLastError(), "paged select");
+    e = launch_overlapped(score_kernel<T, LP, NC>, sms, kThreads, lens, st, m, (const T*)q, q_stride, (const T*)k_bounds,
+                          table, seq_len, n_select, keep_first, keep_last, (uint2*)ws, status);
+    if (e == cudaSuccess)
+        e = launch_overlapped(pick, m.n_seqs * m.hkv, kThreads, sizeof(uint32_t) * std::min(m.max_pages, kInShared), st, m,
+                              (const T*)q, q_stride, (const T*)k_bounds, table, seq_len, n_select, keep_first,
+                              keep_last, (uint2*)ws, pages, status);
+    return note_error(e, "paged select");
 }
 
 }  // namespace
