@@ -5,6 +5,7 @@
 """
 from __future__ import annotations
 
+import ctypes
 import threading
 from typing import Optional
 
@@ -15,6 +16,8 @@ from .binding import EINVAL, SplitKVError
 
 _COUNTERS = 4096  # bytes at the head of the workspace that have to be zero before its first use
 _MOST = (1 << 31) - 1
+_I32, _F32 = torch.int32, torch.float32
+_append, _select, _decode = B._lib.splitkv_paged_append, B._lib.splitkv_paged_select, B._lib.splitkv_paged_decode
 
 # torch.cuda.current_device() and current_stream(device).cuda_stream, without the objects around them.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -81,29 +84,32 @@ class PagedKV:
         self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), shape[1], shape[3]
         self.page_size, self.max_seqs, self.max_pages = shape[2], int(max_seqs), int(max_pages)
         self._scale = scale
-        self._q_shape = (self.n_q_heads, self.head_dim)
-        self._kv_shape = (self.n_kv_heads, self.head_dim)
+        self._dev = k_cache.get_device()  # -1 on the CPU
+        self._index = self._dev if self.device.type == "cuda" else None
         self._layouts = {}  # (table width, table stride) -> splitkv_paged
-        size = B.splitkv_paged_workspace_size(self._layout(self.max_pages, self.max_pages), self.max_seqs)
-        if size == 0:  # let the library say what is wrong with the description
-            B.splitkv_paged_decode(self._layout(self.max_pages, self.max_pages), self.max_seqs, None, 0, None, None, None,
-                                   None, None, 0, None, None, None, None, stream=0)
-        self._ws_bytes = size
-        self._ws = self._stream = None
+        whole = self._layout(self.max_pages, self.max_pages)
+        self._ws_bytes = B._lib.splitkv_paged_workspace_size(whole, self.max_seqs)
+        if self._ws_bytes == 0:  # let the library say what is wrong with the description
+            raise SplitKVError(_decode(whole, self.max_seqs, *[0] * 14), "PagedKV")
+        self.status = torch.zeros(1, dtype=_I32, device=self.device)
+        # The object's own tensors, which it keeps.
+        self._k_at, self._v_at, self._status_at = k_cache.data_ptr(), v_cache.data_ptr(), self.status.data_ptr()
+        self._bounds_at = None if k_bounds is None else k_bounds.data_ptr()
         self._lock = threading.Lock()
-        self._index = self.device.index if self.device.type == "cuda" else None
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        if self.device.type == "cuda":
-            self._ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
+        self._ws = self._stream = None
+        if self._index is not None:
+            self._ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
+            self._ws_at = self._ws.data_ptr()
             self._stream = torch.cuda.current_stream(self.device)
 
-    # -- marshalling (texts are made only where a check fails: these calls are made once per layer and token)
-    def _layout(self, width: int, stride: int) -> B.Paged:
+    # -- marshalling. These calls are made once per layer and token: checks are plain comparisons, texts are made only where
+    # one fails, and the library is called with integers.
+    def _layout(self, width: int, stride: int):
         got = self._layouts.get((width, stride))
         if got is None:
             st = self.k_cache.stride()
-            got = B.make_paged(self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.k_cache.shape[0],
-                               width, st[:3], stride, self._scale, self.dtype)
+            got = ctypes.byref(B.make_paged(self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size,
+                                            self.k_cache.shape[0], width, st[:3], stride, self._scale, self.dtype))
             if len(self._layouts) < 64:
                 self._layouts[(width, stride)] = got
         return got
@@ -122,7 +128,7 @@ class PagedKV:
             return fn(*args)
 
     def _table(self, page_table, what):
-        if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != self.device or
+        if (page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.get_device() != self._dev or
                 (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
             raise SplitKVError(EINVAL, f"{what}: page_table must be an int32 [n_seqs, pages] tensor on the cache's "
                                "device, its rows dense")
@@ -134,21 +140,21 @@ class PagedKV:
         return n, self._layout(width, stride)
 
     def _list(self, t, n, what, name):
-        if t.dtype != torch.int32 or t.shape != (n,) or t.device != self.device or not t.is_contiguous():
+        if t.dtype is not _I32 or t.shape != (n,) or t.get_device() != self._dev or not t.is_contiguous():
             raise SplitKVError(EINVAL, f"{what}: {name} must be a dense int32 [{n}] tensor on the cache's device")
 
-    def _rows(self, t, n, shape, what, name) -> int:
+    def _rows(self, t, n, heads, what, name) -> int:
         """Stride between the tokens of a [n, heads, head_dim] tensor whose heads are dense."""
-        heads, d = shape
-        if t.dtype == self.dtype and t.shape == (n, heads, d) and t.device == self.device:
-            st = t.stride()
-            if st[2] == 1 and (heads == 1 or st[1] == d):
-                return st[0] if n > 1 else heads * d
+        d = self.head_dim
+        if t.dtype is self.dtype and t.shape == (n, heads, d) and t.get_device() == self._dev:
+            token, head, one = t.stride()
+            if one == 1 and (head == d or heads == 1):
+                return token if n > 1 else heads * d
         raise SplitKVError(EINVAL, f"{what}: {name} must be a {self.dtype} [{n}, {heads}, {d}] tensor on the cache's "
                            "device, each token's heads dense")
 
     def _out(self, t, shape, dtype, what, name):
-        if t.shape != shape or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != self._dev or not t.is_contiguous():
             raise SplitKVError(EINVAL, f"{what}: {name} must be a dense {dtype} tensor of {shape} on the cache's device")
 
     # -- the calls
@@ -162,28 +168,33 @@ class PagedKV:
         what = "PagedKV.append"
         n = k.shape[0] if k.dim() else 0
         n_seqs, layout = self._table(page_table, what)
-        ks = self._rows(k, n, self._kv_shape, what, "k")
-        vs = self._rows(v, n, self._kv_shape, what, "v")
+        ks = self._rows(k, n, self.n_kv_heads, what, "k")
+        vs = self._rows(v, n, self.n_kv_heads, what, "v")
         self._list(token_seq, n, what, "token_seq")
         self._list(token_pos, n, what, "token_pos")
         qs = rope_len = rope_dim = 0
         if rope is not None:
-            if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != self.device or not rope.is_contiguous():
+            if rope.dtype is not _F32 or rope.dim() != 2 or rope.get_device() != self._dev or not rope.is_contiguous():
                 raise SplitKVError(EINVAL, f"{what}: rope must be a dense float32 [positions, rope_dim] tensor")
             rope_len, rope_dim = rope.shape
         if q is not None:
-            qs = self._rows(q, n, self._q_shape, what, "q")
+            qs = self._rows(q, n, self.n_q_heads, what, "q")
         elif q_out is not None:
             raise SplitKVError(EINVAL, f"{what}: q_out without q")
         if q_out is not None:
-            self._out(q_out, (n, *self._q_shape), self.dtype, what, "q_out")
-        if stream is not None or self._index is None or _current_device() != self._index:
+            self._out(q_out, (n, self.n_q_heads, self.head_dim), self.dtype, what, "q_out")
+        index = self._index
+        if stream is not None or index is None or _current_device() != index:
             return self._on(self.append, stream, k, v, page_table, token_seq, token_pos, q, rope, interleaved, q_out)
         if q is not None and q_out is None:
-            q_out = q.new_empty((n, *self._q_shape))
-        B.splitkv_paged_append(layout, n_seqs, n, q, qs, k, ks, v, vs, rope, rope_dim, rope_len, 1 if interleaved else 0,
-                               page_table, token_seq, token_pos, q_out, self.k_cache, self.v_cache, self.k_bounds,
-                               self.status, _raw_stream(self._index))
+            q_out = q.new_empty((n, self.n_q_heads, self.head_dim))
+        rc = _append(layout, n_seqs, n, None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                     None if rope is None else rope.data_ptr(), rope_dim, rope_len, 1 if interleaved else 0,
+                     page_table.data_ptr(), token_seq.data_ptr(), token_pos.data_ptr(),
+                     None if q is None else q_out.data_ptr(), self._k_at, self._v_at, self._bounds_at, self._status_at,
+                     _raw_stream(index))
+        if rc:
+            raise SplitKVError(rc, "splitkv_paged_append")
         return q_out
 
     def select(self, q, page_table, seq_lens, n_select, keep_first=1, keep_last=1, pages=None, stream=None):
@@ -194,24 +205,27 @@ class PagedKV:
         if self.k_bounds is None:
             raise SplitKVError(EINVAL, f"{what}: the cache has no bounds (PagedKV(..., bounds=True))")
         n, layout = self._table(page_table, what)
-        qs = self._rows(q, n, self._q_shape, what, "q")
+        qs = self._rows(q, n, self.n_q_heads, what, "q")
         self._list(seq_lens, n, what, "seq_lens")
         n_select = int(n_select)
         if n_select < 1 or keep_first < 0 or keep_last < 0:
             raise SplitKVError(EINVAL, f"{what}: n_select, keep_first, keep_last")
         shape = (n, self.n_kv_heads, n_select)
         if pages is not None:
-            self._out(pages, shape, torch.int32, what, "pages")
-        if stream is not None or self._index is None or _current_device() != self._index:
+            self._out(pages, shape, _I32, what, "pages")
+        index = self._index
+        if stream is not None or index is None or _current_device() != index:
             return self._on(self.select, stream, q, page_table, seq_lens, n_select, keep_first, keep_last, pages)
         if pages is None:
             pages = seq_lens.new_empty(shape)
         # Scratch of the call alone: 8 bytes per page and kv head. No sequence has more pages than its row: any larger
         # number of kept ones says the same.
         ws = seq_lens.new_empty((n * self.n_kv_heads * page_table.shape[1] * 2 + 4,))
-        B.splitkv_paged_select(layout, n, q, qs, self.k_bounds, page_table, seq_lens, n_select,
-                               min(int(keep_first), _MOST), min(int(keep_last), _MOST), pages, self.status, ws,
-                               _raw_stream(self._index))
+        rc = _select(layout, n, q.data_ptr(), qs, self._bounds_at, page_table.data_ptr(), seq_lens.data_ptr(), n_select,
+                     min(int(keep_first), _MOST), min(int(keep_last), _MOST), pages.data_ptr(), self._status_at,
+                     ws.data_ptr(), ws.shape[0] * 4, _raw_stream(index))
+        if rc:
+            raise SplitKVError(rc, "splitkv_paged_select")
         return pages
 
     def decode(self, q, page_table, seq_lens, pages=None, o=None, lse=None, stream=None):
@@ -221,41 +235,45 @@ class PagedKV:
         of a sequence, list its row once for each, with the length that the token sees."""
         what = "PagedKV.decode"
         n, layout = self._table(page_table, what)
-        qs = self._rows(q, n, self._q_shape, what, "q")
+        heads = self.n_q_heads
+        qs = self._rows(q, n, heads, what, "q")
         self._list(seq_lens, n, what, "seq_lens")
-        n_select = 0
+        n_select, pages_at = 0, None
         if pages is not None:
             n_select = pages.shape[2] if pages.dim() == 3 else 0
             if n_select < 1:
                 raise SplitKVError(EINVAL, f"{what}: pages must be [n_seqs, n_kv_heads, n_select]")
-            self._out(pages, (n, self.n_kv_heads, n_select), torch.int32, what, "pages")
+            self._out(pages, (n, self.n_kv_heads, n_select), _I32, what, "pages")
+            pages_at = pages.data_ptr()
         if o is not None:
-            self._out(o, (n, *self._q_shape), self.dtype, what, "o")
+            self._out(o, (n, heads, self.head_dim), self.dtype, what, "o")
         if lse is not None:
-            self._out(lse, (n, self.n_q_heads), torch.float32, what, "lse")
+            self._out(lse, (n, heads), _F32, what, "lse")
         index = self._index
         if stream is not None or index is None or _current_device() != index:
             return self._on(self.decode, stream, q, page_table, seq_lens, pages, o, lse)
         if o is None:
-            o = q.new_empty((n, *self._q_shape))
+            o = torch.empty_like(q) if q.is_contiguous() else q.new_empty((n, heads, self.head_dim))
         if lse is None:
-            lse = q.new_empty((n, self.n_q_heads), dtype=torch.float32)
+            lse = q.new_empty((n, heads), dtype=_F32)
         raw = _raw_stream(index)
+        args = (layout, n, q.data_ptr(), qs, self._k_at, self._v_at, page_table.data_ptr(), seq_lens.data_ptr(), pages_at,
+                n_select, o.data_ptr(), lse.data_ptr(), self._status_at)
         if torch._C._cuda_isCurrentStreamCapturing():
             # The graph may be replayed beside other work of this object: scratch of its own, its counters zeroed
             # by the graph.
             ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             ws[:_COUNTERS].zero_()
-            B.splitkv_paged_decode(layout, n, q, qs, self.k_cache, self.v_cache, page_table, seq_lens, pages, n_select,
-                                   o, lse, self.status, ws, raw)
-            return o, lse
-        with self._lock:
-            if raw != self._stream.cuda_stream:  # the scratch is used in turn
-                now = torch.cuda.current_stream(self.device)
-                now.wait_stream(self._stream)
-                self._stream = now
-            B.splitkv_paged_decode(layout, n, q, qs, self.k_cache, self.v_cache, page_table, seq_lens, pages, n_select,
-                                   o, lse, self.status, self._ws, raw)
+            rc = _decode(*args, ws.data_ptr(), self._ws_bytes, raw)
+        else:
+            with self._lock:
+                if raw != self._stream.cuda_stream:  # the scratch is used in turn
+                    now = torch.cuda.current_stream(self.device)
+                    now.wait_stream(self._stream)
+                    self._stream = now
+                rc = _decode(*args, self._ws_at, self._ws_bytes, raw)
+        if rc:
+            raise SplitKVError(rc, "splitkv_paged_decode")
         return o, lse
 
     # -- host-side reads (synchronizing; for tests and reports)
