@@ -447,8 +447,10 @@ int build_paged(const splitkv_paged* p, int64_t n_seqs, PagedMeta* m) {
     if (p->page_size > 1024 || (p->page_size & (p->page_size - 1))) return SPLITKV_EUNSUPPORTED;
     if (p->n_pages > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX) return SPLITKV_EUNSUPPORTED;
     if (n_seqs > SPLITKV_PAGED_MAX_SEQS || p->n_q_heads > 32768) return SPLITKV_EUNSUPPORTED;
-    // The units of work (16 positions of a sequence and kv head) are counted in 64 bits, those of one head in 32.
-    if (n_seqs * (((int64_t)p->max_pages * p->page_size + 15) / 16 + 4) > INT32_MAX) return SPLITKV_EUNSUPPORTED;
+    // The units of work (16 positions of a sequence, kv head and 8 query rows) are counted in 31 bits.
+    if (n_seqs * (((int64_t)p->max_pages * p->page_size + 15) / 16 + 4) >
+        INT32_MAX / ((int64_t)p->n_kv_heads * ((p->n_q_heads / p->n_kv_heads + 7) / 8)))
+        return SPLITKV_EUNSUPPORTED;
     if (p->page_stride % vec || p->head_stride % vec || p->token_stride % vec) return SPLITKV_EINVAL;
     // No two rows of the cache may overlap: by ascending stride, each step goes past what the smaller ones cover.
     std::pair<int64_t, int64_t> dim[3] = {

@@ -31,6 +31,7 @@ constexpr int kSegmentCost = 4;    // units that the beginning of a segment coun
 constexpr int kAlone = 6;          // tiles a warp may have for a block to take a whole segment, without a join of blocks
 constexpr float kLazy = 8.f;       // log2 units a score may exceed the reference before the reference moves
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kNone = ~0u;
 constexpr int kMaxDP = 128, kMaxRows = 16;
 
 static_assert(kMaxParts * sizeof(uint32_t) <= kCounterBytes, "counters");
@@ -340,42 +341,34 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
 }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 
-// a / b for values that nearly always fit 32 bits.
-__device__ __noinline__ int64_t div_wide(int64_t a, int64_t b) { return a / b; }
-__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : div_wide(a, b);
-}
-
-// The line of units. A segment (sequence, kv head, group of query rows) takes kSegmentCost units before its tiles': what
-// it costs to begin one (table, queries, first keys: one after the other) next to the streaming of a tile.
+// The line of units (fewer than 2^31: the entry point sees to it). A segment (sequence, kv head, group of query rows)
+// takes kSegmentCost units before its tiles': what it costs to begin one (table, queries, first keys: one after the
+// other) next to the streaming of a tile.
 struct Line {
-    const int32_t* prefix;    // shared: units of the sequences before b, for one segment of each
-    int32_t n_seqs, per_seq;  // per_seq = kv heads x groups of query rows: segments of a sequence
-    int64_t total, per_part;
-
-    __device__ __forceinline__ int32_t part_of(int64_t u) const { return (int32_t)div_units(u, per_part); }
+    const uint32_t* prefix;    // shared: units of the sequences before b, for one segment of each
+    uint32_t n_seqs, per_seq;  // per_seq = kv heads x groups of query rows: segments of a sequence
+    uint32_t total, per_part;
 };
 
 struct Segment {
     int32_t b, sub, tiles;  // sequence, kv head and row group, tiles
-    int64_t start;          // first unit; its tiles begin at start + kSegmentCost
-    __device__ __forceinline__ int64_t tile0() const { return start + kSegmentCost; }
-    __device__ __forceinline__ int64_t end() const { return start + kSegmentCost + tiles; }
+    uint32_t start;         // first unit; its tiles begin at start + kSegmentCost
+    __device__ __forceinline__ uint32_t tile0() const { return start + kSegmentCost; }
+    __device__ __forceinline__ uint32_t end() const { return start + kSegmentCost + tiles; }
 };
 
-__device__ __forceinline__ Segment segment_at(const Line& L, int64_t u) {
-    int32_t lo = 0, hi = L.n_seqs;  // the last b with prefix[b] * per_seq <= u
-    while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if ((int64_t)L.prefix[mid] * L.per_seq <= u) lo = mid; else hi = mid;
+__device__ __forceinline__ Segment segment_at(const Line& L, uint32_t u) {
+    uint32_t lo = 0;  // the last b with prefix[b] * per_seq <= u
+    for (uint32_t hi = L.n_seqs; hi - lo > 1;) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (L.prefix[mid] * L.per_seq <= u) lo = mid; else hi = mid;
     }
-    const int32_t width = L.prefix[lo + 1] - L.prefix[lo];
-    const int64_t base = (int64_t)L.prefix[lo] * L.per_seq;
+    const uint32_t base = L.prefix[lo], width = L.prefix[lo + 1] - base;
     Segment s;
     s.b = lo;
     s.tiles = width - kSegmentCost;
-    s.sub = (int32_t)div_units(u - base, width);
-    s.start = base + (int64_t)s.sub * width;
+    s.sub = (u - base * L.per_seq) / width;
+    s.start = base * L.per_seq + s.sub * width;
     return s;
 }
 
@@ -414,13 +407,13 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     using P = Partial<DP, R>;
     extern __shared__ __align__(16) char smem[];
     P* part = reinterpret_cast<P*>(smem);  // [W][2]: a warp's part of the segment it entered, of the one it left
-    __shared__ int64_t seg_of[2 * W];      // first unit of the segment that part belongs to, -1: none
+    __shared__ uint32_t seg_of[2 * W];     // first unit of the segment that part belongs to, kNone: none
     __shared__ int32_t list[2 * W];        // the parts there are
     __shared__ float weight[2 * W][R];
     __shared__ float scale_of[2 * W][R];   // 1 / sum of a finished row
     __shared__ Group group[2 * W];
     __shared__ Side side[2];
-    int32_t* prefix = reinterpret_cast<int32_t*>(smem + sizeof(P) * W * 2);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + sizeof(P) * W * 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row_groups = (m.group + R - 1) / R;
 
@@ -434,7 +427,7 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         if (pages) n = min(n_select, (len + m.page - 1) >> m.page_shift) << m.page_shift;
         return n ? (n + kTile - 1) / kTile + kSegmentCost : 0;
     };
-    if (lane < 2) seg_of[warp * 2 + lane] = -1;
+    if (lane < 2) seg_of[warp * 2 + lane] = kNone;
     bool empties;      // some sequence has no keys
     int32_t widest;    // units of the longest segment
     if (m.n_seqs <= 32) {  // each warp by itself
@@ -478,9 +471,9 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         __syncthreads();
     }
     const bool skip = __any_sync(0xffffffffu, bad);
-    Line L{prefix, m.n_seqs, m.hkv * row_groups, 0, 0};
-    L.total = (int64_t)prefix[m.n_seqs] * L.per_seq;
-    L.per_part = max(div_units(L.total + gridDim.x - 1, gridDim.x), (int64_t)W);
+    Line L{prefix, (uint32_t)m.n_seqs, (uint32_t)(m.hkv * row_groups), 0, 0};
+    L.total = prefix[m.n_seqs] * L.per_seq;
+    L.per_part = max((L.total - 1) / gridDim.x + 1, (uint32_t)W);
 
     // ---- sequences without keys
     if (empties && !skip)
@@ -492,25 +485,26 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
                 for (int i = tid; i < m.hkv * n_select; i += kThreads)
                     if (pages[(int64_t)b * m.hkv * n_select + i] != -1) raise_status(status, SPLITKV_DEV_BAD_PAGE);
         }
-    int64_t c_lo = (int64_t)blockIdx.x * L.per_part, c_hi = min(c_lo + L.per_part, L.total);
-    if (widest <= kAlone * W && (int64_t)m.n_seqs * L.per_seq <= gridDim.x) {  // a block per segment
-        const int b = blockIdx.x / L.per_seq;
-        if (b >= m.n_seqs) return;
-        const int32_t width = prefix[b + 1] - prefix[b];
-        c_lo = (int64_t)prefix[b] * L.per_seq + (int64_t)(blockIdx.x - b * L.per_seq) * width;
+    // This block's part [c_lo, c_hi) of the line, and each warp's part of it.
+    uint32_t c_lo = min(blockIdx.x * L.per_part, L.total), c_hi = min(c_lo + L.per_part, L.total);
+    if (widest <= kAlone * W && L.n_seqs * L.per_seq <= gridDim.x) {  // a block per segment
+        const uint32_t b = blockIdx.x / L.per_seq;
+        if (b >= L.n_seqs) return;
+        const uint32_t width = prefix[b + 1] - prefix[b];
+        c_lo = prefix[b] * L.per_seq + (blockIdx.x - b * L.per_seq) * width;
         c_hi = c_lo + width;
     }
     if (c_lo >= c_hi) return;
-    const int64_t units = c_hi - c_lo;
-    const int64_t w_lo = c_lo + units * warp / W, w_hi = c_lo + units * (warp + 1) / W;
+    const uint32_t each = (c_hi - c_lo) / W, more = (c_hi - c_lo) % W;
+    const uint32_t w_lo = c_lo + warp * each + min((uint32_t)warp, more), w_hi = w_lo + each + ((uint32_t)warp < more);
 
     Frag<T, DP, NT> f;
     const float to_log2 = m.scale * kLog2e;
-    for (int64_t u = skip ? w_hi : w_lo; u < w_hi;) {
+    for (uint32_t u = skip ? w_hi : w_lo; u < w_hi;) {
         const Segment sg = segment_at(L, u);
-        const int32_t t_begin = (int32_t)max(u - sg.tile0(), (int64_t)0);
+        const int32_t t_begin = max((int32_t)(u - sg.tile0()), 0);
         u = min(w_hi, sg.end());
-        const int32_t t_end = (int32_t)max(u - sg.tile0(), (int64_t)0);
+        const int32_t t_end = max((int32_t)(u - sg.tile0()), 0);
         if (t_end <= t_begin) continue;  // of this segment's units only those of its beginning
         const int32_t g = sg.sub / row_groups, row0 = (sg.sub - g * row_groups) * R;
         const int32_t rows = min(R, m.group - row0);
@@ -662,8 +656,8 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
             const int32_t g = sg.sub / row_groups, row0 = (sg.sub - g * row_groups) * R;
             Side x{0, 0, min(R, m.group - row0), 0, (int64_t)sg.b * m.hq + g * m.group + row0};
             if (open) {
-                x.first = L.part_of(sg.tile0());
-                x.n = L.part_of(sg.end() - 1) - x.first + 1;
+                x.first = sg.tile0() / L.per_part;
+                x.n = (sg.end() - 1) / L.per_part - x.first + 1;
             }
             side[warp] = x;
         }
@@ -674,12 +668,12 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     P* const mine = reinterpret_cast<P*>(slots) + blockIdx.x * 2;
     int n_groups;
     {
-        const int64_t of = lane < 2 * W ? seg_of[lane] : -1;
-        const uint32_t valid = __ballot_sync(0xffffffffu, of >= 0), below = valid & ((1u << lane) - 1);
-        const int64_t before = __shfl_sync(0xffffffffu, of, below ? 31 - __clz(below) : 0);
-        const uint32_t heads = __ballot_sync(0xffffffffu, of >= 0 && (!below || before != of));
+        const uint32_t of = lane < 2 * W ? seg_of[lane] : kNone;
+        const uint32_t valid = __ballot_sync(0xffffffffu, of != kNone), below = valid & ((1u << lane) - 1);
+        const uint32_t before = __shfl_sync(0xffffffffu, of, below ? 31 - __clz(below) : 0);
+        const uint32_t heads = __ballot_sync(0xffffffffu, of != kNone && (!below || before != of));
         n_groups = __popc(heads);
-        if (warp == 0 && of >= 0) list[__popc(below)] = lane;
+        if (warp == 0 && of != kNone) list[__popc(below)] = lane;
         for (int k = warp; k < n_groups; k += W) {
             uint32_t rest = heads;
             for (int i = 0; i < k; ++i) rest &= rest - 1;
@@ -769,6 +763,18 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         float* wt = reinterpret_cast<float*>(smem);  // [n][R]: maxima, then weights
         float* ls = wt + kMaxParts * R;              // [n][R]: sums
         float* inv = ls + kMaxParts * R;             // [R]
+        // The first parts' values are asked for before their weights are known.
+        constexpr int kAhead = 16;
+        float4 z[kAhead];
+        auto load = [&](int x, int k0) {
+            const float* p = &all[2 * k0].o[0][0] + x * 4;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                z[k] = x < S.rows * kCols && k0 + k < S.n
+                           ? __ldcg(reinterpret_cast<const float4*>(p + (2 * k + (k0 + k == 0)) * (sizeof(P) / 4)))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        load(tid, 0);
         for (int x = tid; x < S.n * R; x += kThreads) {
             const int k = x / R, row = x % R;
             if (row >= S.rows) continue;
@@ -796,12 +802,15 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         __syncthreads();
         for (int x = tid; x < S.rows * kCols; x += kThreads) {
             const int row = x / kCols, c = x % kCols * 4;
+            if (x != tid) load(x, 0);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < S.n; ++k) {
-                const float4 z = __ldcg(reinterpret_cast<const float4*>(&all[2 * k + (k == 0)].o[row][c]));
-                const float w = wt[k * R + row];
-                acc.x += w * z.x, acc.y += w * z.y, acc.z += w * z.z, acc.w += w * z.w;
+            for (int k0 = 0; k0 < S.n; k0 += kAhead) {
+                if (k0) load(x, k0);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const float w = k0 + k < S.n ? wt[(k0 + k) * R + row] : 0.f;
+                    acc.x += w * z[k].x, acc.y += w * z[k].y, acc.z += w * z[k].z, acc.w += w * z[k].w;
+                }
             }
             const float i = inv[row];
             if (c < m.d) store4(o + (S.h + row) * m.d + c, make_float4(acc.x * i, acc.y * i, acc.z * i, acc.w * i));
