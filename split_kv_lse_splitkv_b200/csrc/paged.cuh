@@ -59,9 +59,10 @@ cudaError_t sm_count(int* sms);
 using SmemGrants = std::atomic<bool>[kMaxDevices];
 cudaError_t allow_smem(const void* kernel, size_t most, SmemGrants& granted);
 
-// Launch in which the kernel may be placed on the SMs while the one before it in the stream drains: it begins with
-// after_previous(), which waits until that one has completed and its writes are seen. Hides the launch's own latency
-// (2 us of every call), which is felt where a call takes ten.
+// Launch in which the kernel may be placed on the SMs while the one before it in the stream drains. Every thread of it
+// calls after_previous(), which waits until that one has completed and its writes are seen, before it touches memory; or,
+// in the second kernel of a call, before it touches what the first one writes (the call's inputs are there once the first
+// one has let its dependents start). Hides the launch's own latency (2 us of every call), felt where a call takes ten.
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};
@@ -77,8 +78,8 @@ cudaError_t launch_overlapped(void (*kernel)(P...), int64_t grid, int threads, s
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 __device__ __forceinline__ void after_previous() {
-    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Length of sequence b, or 0 (with the status bit) when it is not in [0, max_pages * page].

@@ -217,49 +217,206 @@ struct Angles {
     }
 };
 
-__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// kAhead rows a lane: rows (heads) h, h + L.rows, .. below h1.
+template <typename T, int kAhead>
+struct Rows {
+    uint4 x[kAhead], y[kAhead];
+    __device__ __forceinline__ void load(const PagedMeta& m, const Lanes& L, const T* src, int h, int h1) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = (int64_t)(h + k * L.rows) * m.d;
+            const bool in = L.row < L.rows && h + k * L.rows < h1;
+            x[k] = ldg_stream_if(src + at + L.a, in);
+            y[k] = ldg_stream_if(src + at + L.b, in && L.b >= 0);
+        }
+    }
+    __device__ __forceinline__ void store(const AppendArgs& a, const Lanes& L, T* dst, int64_t step, int h, int h1,
+                                          const Angles<T>* turn) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (L.row >= L.rows || h + k * L.rows >= h1) continue;
+            if (turn) turn->turn(x[k], y[k], a.interleaved);
+            T* row = dst + (h + k * L.rows) * step;
+            *reinterpret_cast<uint4*>(row + L.a) = x[k];
+            if (L.b >= 0) *reinterpret_cast<uint4*>(row + L.b) = y[k];
+        }
+    }
+};
 
-// Queries of one token: heads [h0, h1), a warp.
-template <typename T>
+// Queries of one token, heads [h0, h1), on a warp. The first rows are asked for before the token's position is known.
+template <typename T, int kAhead>
 __device__ __forceinline__ void append_queries(const PagedMeta& m, const AppendArgs& a, int64_t i, int h0, int h1,
-                                               int lane, int32_t* status) {
+                                               int lane) {
     const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    const T* src = (const T*)a.q + i * a.q_stride;
+    Rows<T, kAhead> r;
+    r.load(m, L, src, h0 + L.row, h1);
     const int32_t seq = __ldg(a.token_seq + i), pos = __ldg(a.token_pos + i);
     // A token that is out of range is reported with its keys; its queries pass as they are.
     const bool turn = L.pair >= 0 && seq >= 0 && pos >= 0 && pos < a.rope_len;
     Angles<T> ang;
     if (turn) ang.load(a.rope + (int64_t)pos * a.rope_dim, a.rope_dim / 2, L.pair);
-    const T* src = (const T*)a.q + i * a.q_stride;
-    T* dst = (T*)a.q_out + i * m.hq * m.d;
-    if (L.row >= L.rows) return;
-    constexpr int kAhead = 4;
-    for (int h = h0 + L.row; h < h1; h += kAhead * L.rows) {
-        uint4 x[kAhead], y[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int64_t at = (int64_t)(h + k * L.rows) * m.d;
-            if (h + k * L.rows >= h1) continue;
-            x[k] = ldg16(src + at + L.a);
-            if (L.b >= 0) y[k] = ldg16(src + at + L.b);
+    for (int h = h0;;) {
+        r.store(a, L, (T*)a.q_out + i * m.hq * m.d, m.d, h + L.row, h1, turn ? &ang : nullptr);
+        if ((h += kAhead * L.rows) >= h1) break;
+        r.load(m, L, src, h + L.row, h1);
+    }
+}
+
+// Whether token i, of sequence seq >= 0, comes after the token before it that is not padding (else the status bit).
+__device__ __forceinline__ void check_order(const AppendArgs& a, int64_t i, int32_t seq, int32_t pos, int32_t* status,
+                                            int32_t& before, int32_t& before_pos) {
+    before = before_pos = -1;
+    for (int64_t p = i - 1; p >= 0; --p)
+        if ((before = __ldg(a.token_seq + p)) >= 0) {
+            before_pos = __ldg(a.token_pos + p);
+            break;
         }
+    if (before > seq || (before == seq && before_pos >= pos)) raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
+}
+
+// Many tokens: every token's rows by themselves; a warp has `heads` heads of its queries, or half as many of its keys and
+// values. The bounds of the keys follow in a launch of their own, from L2. (A page's rows and bounds in one block, as
+// below, keep too few loads in flight to fill the GPU: 35k tokens took 52 us for keys and values alone, against
+// 23 us for their bytes.)
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status,
+                                                                    int32_t heads) {
+    after_previous();
+    if (status_bad(status)) return;
+    const int lane = threadIdx.x & 31;
+    const int32_t q_units = a.q ? (m.hq + heads - 1) / heads : 0, kv_heads = heads / 2;
+    const int32_t per_token = q_units + (m.hkv + kv_heads - 1) / kv_heads;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), i = unit / per_token;
+    if (i >= a.n_tokens) return;
+    const int32_t j = (int32_t)(unit - i * per_token);
+    if (j < q_units) {
+        append_queries<T, 2>(m, a, i, j * heads, min((j + 1) * heads, m.hq), lane);
+        return;
+    }
+    const int32_t h0 = (j - q_units) * kv_heads, h1 = min(h0 + kv_heads, m.hkv);
+    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    Rows<T, 2> k, v;
+    k.load(m, L, (const T*)a.k + i * a.k_stride, h0 + L.row, h1);
+    v.load(m, L, (const T*)a.v + i * a.v_stride, h0 + L.row, h1);
+    const TokenPlace t = token_place(m, a, i, status);
+    if (j == q_units && lane == 0 && t.seq >= 0) {
+        int32_t before, before_pos;
+        check_order(a, i, t.seq, t.pos, status, before, before_pos);
+    }
+    if (t.page < 0) return;
+    Angles<T> ang;
+    if (L.pair >= 0) ang.load(a.rope + (int64_t)t.pos * a.rope_dim, a.rope_dim / 2, L.pair);
+    const int64_t at = paged_row(m, t.page, 0, t.pos & (m.page - 1));
+    k.store(a, L, (T*)a.k_cache + at, m.head_stride, h0 + L.row, h1, L.pair >= 0 ? &ang : nullptr);
+    v.store(a, L, (T*)a.v_cache + at, m.head_stride, h0 + L.row, h1, nullptr);
+}
+
+// Which of the 32 tokens from i0 on (a lane each) are the first of the call in their page. `report`: say what is wrong
+// with them, in the status word.
+__device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const AppendArgs& a, int64_t i0, int32_t slice,
+                                                int lane, bool report, int32_t* status) {
+    const int64_t i = i0 + lane;
+    const bool mine = lane < slice && i < a.n_tokens;
+    const int32_t seq = mine ? __ldg(a.token_seq + i) : -1, pos = seq >= 0 ? __ldg(a.token_pos + i) : 0;
+    bool first = seq >= 0;
+    if (first) {
+        int32_t before, before_pos;
+        check_order(a, i, seq, pos, report ? status : nullptr, before, before_pos);
+        if (seq >= m.n_seqs || pos < 0 || pos >= (int64_t)m.max_pages * m.page || (a.rope && pos >= a.rope_len)) {
+            if (report) raise_status(status, SPLITKV_DEV_BAD_TOKEN);
+            first = false;
+        } else if (before == seq && before_pos >= 0 && before_pos >> m.page_shift == pos >> m.page_shift) {
+            first = false;
+        }
+    }
+    return __ballot_sync(0xffffffffu, first);
+}
+
+// Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's 32, at one kv head.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * 32;
+    const int32_t g = (int32_t)(unit % m.hkv);
+    const Lanes L = lanes_of<T>(m.d, 0, 0, lane);
+    uint32_t firsts = page_firsts(m, a, i0, 32, lane, false, status);
+    bool waited = false;
+    if (!firsts) after_previous();
+    for (; firsts; firsts &= firsts - 1) {
+        const int64_t i = i0 + __ffs(firsts) - 1;
+        const int32_t seq = __ldg(a.token_seq + i), entry = __ldg(a.token_pos + i) >> m.page_shift;
+        const int32_t page = paged_page(m, a.table + seq * m.table_stride, entry, status);
+        int32_t last = 0;  // the last of the page's tokens: they go on to the first token of another page
+        for (int64_t base = i;; base += 32) {
+            const int64_t t = base + lane;
+            const int32_t s = t < a.n_tokens ? __ldg(a.token_seq + t) : INT32_MAX;
+            const int32_t q = s >= 0 && s < INT32_MAX ? __ldg(a.token_pos + t) : -1;
+            const bool in = s == seq && q >= 0 && q >> m.page_shift == entry;
+            const uint32_t stops = __ballot_sync(0xffffffffu, s >= 0 && !in);
+            const int end = stops ? __ffs(stops) - 1 : 32;
+            last = max(last, __reduce_max_sync(0xffffffffu, in && lane < end ? q & (m.page - 1) : 0));
+            if (stops) break;
+        }
+        if (!waited) after_previous();  // the keys
+        waited = true;
+        if (page < 0 || __any_sync(0xffffffffu, status_bad(status))) continue;
+        uint4 lo[2], hi[2];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int64_t at = (int64_t)(h + k * L.rows) * m.d;
-            if (h + k * L.rows >= h1) continue;
-            if (turn) ang.turn(x[k], y[k], a.interleaved);
-            *reinterpret_cast<uint4*>(dst + at + L.a) = x[k];
-            if (L.b >= 0) *reinterpret_cast<uint4*>(dst + at + L.b) = y[k];
+        for (int x = 0; x < 2; ++x) {
+            lo[x] = make_uint4(Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf);
+            hi[x] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
+        }
+        const T* kc = (const T*)a.k_cache + paged_row(m, page, g, 0);
+        constexpr int kAhead = 4;
+        for (int32_t off0 = 0; off0 <= last; off0 += kAhead * L.rows) {
+            uint4 x[kAhead], y[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int32_t off = off0 + u * L.rows + L.row;
+                const bool in = L.row < L.rows && off <= last;
+                x[u] = ldg_stream_if(kc + off * m.token_stride + L.a, in);
+                y[u] = ldg_stream_if(kc + off * m.token_stride + L.b, in && L.b >= 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (L.row >= L.rows || off0 + u * L.rows + L.row > last) continue;
+                take<T, false>(lo[0], x[u]), take<T, true>(hi[0], x[u]);
+                take<T, false>(lo[1], y[u]), take<T, true>(hi[1], y[u]);
+            }
+        }
+        for (int r = 1; r < L.rows; ++r) {  // the lanes of the first row take the others'
+            auto from = [&](const uint4& x) {
+                const int l = (lane + r * L.per_row) & 31;
+                return make_uint4(__shfl_sync(0xffffffffu, x.x, l), __shfl_sync(0xffffffffu, x.y, l),
+                                  __shfl_sync(0xffffffffu, x.z, l), __shfl_sync(0xffffffffu, x.w, l));
+            };
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint4 l = from(lo[x]), h = from(hi[x]);
+                if (lane < L.per_row) take<T, false>(lo[x], l), take<T, true>(hi[x], h);
+            }
+        }
+        if (L.row == 0) {
+            T* dst = (T*)a.k_bounds + ((int64_t)page * m.hkv + g) * 2 * m.d;
+            *reinterpret_cast<uint4*>(dst + L.a) = lo[0];
+            *reinterpret_cast<uint4*>(dst + m.d + L.a) = hi[0];
+            if (L.b >= 0) {
+                *reinterpret_cast<uint4*>(dst + L.b) = lo[1];
+                *reinterpret_cast<uint4*>(dst + m.d + L.b) = hi[1];
+            }
         }
     }
 }
 
 // Blocks [0, kv_blocks): the keys and values of the pages whose first token of the call is one of the block's
-// `slice` tokens. Blocks from there on: queries, `heads` of a token per warp.
+// `slice` tokens, and the pages' bounds. Blocks from there on: queries, `heads` of a token per warp.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArgs a, int32_t* status, int64_t kv_blocks,
                                                           int32_t slice, int32_t heads) {
     constexpr int kN = Vec<T>::kN;
-    __shared__ int32_t tokens[kMaxPage];      // the page's new tokens, from the first one on
+    __shared__ int32_t tokens[kMaxPage];      // the page's new tokens, from the first one on,
+    __shared__ uint16_t offs[kMaxPage];       // and where in the page they go
     __shared__ uint32_t is_new[kMaxPage / 32];
     __shared__ int32_t n_tokens, last_pos;
     __shared__ uint4 red[kWarps][32][4];      // minima and maxima of a lane's two pieces
@@ -271,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
         const int32_t per_token = (m.hq + heads - 1) / heads;
         const int64_t unit = (blockIdx.x - kv_blocks) * kWarps + warp, i = unit / per_token;
         const int32_t h0 = (int32_t)(unit - i * per_token) * heads;
-        if (i < a.n_tokens) append_queries<T>(m, a, i, h0, min(h0 + heads, m.hq), lane, status);
+        if (i < a.n_tokens) append_queries<T, 4>(m, a, i, h0, min(h0 + heads, m.hq), lane);
         return;
     }
 
@@ -279,30 +436,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
     const int v_row = m.d / kN, v_rows = 32 / v_row;  // values: a lane per piece
     // Which of the slice's tokens are the first of a page: a lane per token, the same in every warp.
     const int64_t i0 = blockIdx.x * (int64_t)slice;
-    uint32_t firsts;
-    {
-        const int64_t i = i0 + lane;
-        const bool mine = lane < slice && i < a.n_tokens;
-        const int32_t seq = mine ? __ldg(a.token_seq + i) : -1, pos = seq >= 0 ? __ldg(a.token_pos + i) : 0;
-        bool first = seq >= 0;
-        if (first) {
-            int32_t before = -1, before_pos = -1;
-            for (int64_t p = i - 1; p >= 0; --p)  // padding passed over
-                if ((before = __ldg(a.token_seq + p)) >= 0) {
-                    before_pos = __ldg(a.token_pos + p);
-                    break;
-                }
-            if (warp == 0 && (before > seq || (before == seq && before_pos >= pos)))
-                raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
-            if (seq >= m.n_seqs || pos < 0 || pos >= (int64_t)m.max_pages * m.page || (a.rope && pos >= a.rope_len)) {
-                if (warp == 0) raise_status(status, SPLITKV_DEV_BAD_TOKEN);
-                first = false;
-            } else if (before == seq && before_pos >= 0 && before_pos >> m.page_shift == pos >> m.page_shift) {
-                first = false;
-            }
-        }
-        firsts = __ballot_sync(0xffffffffu, first);
-    }
+    uint32_t firsts = page_firsts(m, a, i0, slice, lane, warp == 0, status);
     for (; firsts; firsts &= firsts - 1) {
         // Every thread of the block takes the same way.
         const int64_t i = i0 + __ffs(firsts) - 1;
@@ -331,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
             const int32_t end = stop;
             if (in && tid < end) {
                 const int32_t k = atomicAdd(&n_tokens, 1), off = q & (m.page - 1);
-                if (k < kMaxPage) tokens[k] = (int32_t)(t - i);
+                if (k < kMaxPage) tokens[k] = (int32_t)(t - i), offs[k] = (uint16_t)off;
                 atomicOr(&is_new[off >> 5], 1u << (off & 31));
                 atomicMax(&last_pos, off);
             }
@@ -353,47 +487,69 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
             }
             T* kc = (T*)a.k_cache + paged_row(m, page, work ? g : 0, 0);
             T* vc = (T*)a.v_cache + paged_row(m, page, work ? g : 0, 0);
-            if (work && L.row < L.rows) {
-                for (int32_t k = sub * L.rows + L.row; k < n; k += subs * L.rows) {
-                    const int64_t t = i + tokens[k];
-                    const int32_t q = __ldg(a.token_pos + t);
-                    const T* src = (const T*)a.k + t * a.k_stride + g * m.d;
-                    uint4 x = ldg16(src + L.a), y = make_uint4(0, 0, 0, 0);
-                    if (L.b >= 0) y = ldg16(src + L.b);
-                    if (L.pair >= 0) {
-                        Angles<T> ang;
-                        ang.load(a.rope + (int64_t)q * a.rope_dim, a.rope_dim / 2, L.pair);
-                        ang.turn(x, y, a.interleaved);
+            // Loads of several rows at a time, then what is done with them.
+            if (work && L.row < L.rows && a.k_bounds) {  // keys that were there
+                constexpr int kAhead = 4;
+                for (int32_t off = sub * L.rows + L.row; off < last; off += kAhead * subs * L.rows) {
+                    uint4 x[kAhead], y[kAhead];
+                    bool in[kAhead];
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const int32_t at = off + u * subs * L.rows;
+                        in[u] = at < last && !(is_new[at >> 5] >> (at & 31) & 1);
+                        const T* src = kc + at * m.token_stride;
+                        x[u] = ldg_stream_if(src + L.a, in[u]);
+                        y[u] = ldg_stream_if(src + L.b, in[u] && L.b >= 0);
                     }
-                    T* dst = kc + (q & (m.page - 1)) * m.token_stride;
-                    *reinterpret_cast<uint4*>(dst + L.a) = x;
-                    take<T, false>(lo[0], x), take<T, true>(hi[0], x);
-                    if (L.b >= 0) {
-                        *reinterpret_cast<uint4*>(dst + L.b) = y;
-                        take<T, false>(lo[1], y), take<T, true>(hi[1], y);
-                    }
-                }
-                if (a.k_bounds) {
-#pragma unroll 4
-                    for (int32_t off = sub * L.rows + L.row; off < last; off += subs * L.rows) {
-                        if (is_new[off >> 5] >> (off & 31) & 1) continue;
-                        const T* src = kc + off * m.token_stride;
-                        const uint4 x = *reinterpret_cast<const uint4*>(src + L.a);
-                        take<T, false>(lo[0], x), take<T, true>(hi[0], x);
-                        if (L.b >= 0) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(src + L.b);
-                            take<T, false>(lo[1], y), take<T, true>(hi[1], y);
-                        }
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        if (!in[u]) continue;
+                        take<T, false>(lo[0], x[u]), take<T, true>(hi[0], x[u]);
+                        take<T, false>(lo[1], y[u]), take<T, true>(hi[1], y[u]);  // (not used where there is no second piece)
                     }
                 }
             }
-            if (work && lane < v_rows * v_row) {
-                const int c = lane % v_row * kN;
-                for (int32_t k = sub * v_rows + lane / v_row; k < n; k += subs * v_rows) {
-                    const int64_t t = i + tokens[k];
-                    const int32_t off = __ldg(a.token_pos + t) & (m.page - 1);
-                    *reinterpret_cast<uint4*>(vc + off * m.token_stride + c) =
-                        ldg16((const T*)a.v + t * a.v_stride + g * m.d + c);
+            // New keys and values together: as many loads in flight as the two have.
+            constexpr int kKeys = 2, kValues = 4;
+            const int c = lane % v_row * kN, steps = kKeys * subs * L.rows, v_steps = kValues * subs * v_rows;
+            int32_t k0 = work && L.row < L.rows ? sub * L.rows + L.row : n;
+            int32_t v0 = work && lane < v_rows * v_row ? sub * v_rows + lane / v_row : n;
+            for (; k0 < n || v0 < n; k0 += steps, v0 += v_steps) {
+                uint4 x[kKeys], y[kKeys], z[kValues];
+                Angles<T> ang[kKeys];
+                int32_t off[kKeys];
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u) {
+                    const int32_t at = k0 + u * subs * L.rows;
+                    const bool in = at < n;
+                    off[u] = in ? offs[at] : -1;
+                    const T* src = (const T*)a.k + (i + (in ? tokens[at] : 0)) * a.k_stride + g * m.d;
+                    x[u] = ldg_stream_if(src + L.a, in);
+                    y[u] = ldg_stream_if(src + L.b, in && L.b >= 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kValues; ++u) {
+                    const int32_t at = v0 + u * subs * v_rows;
+                    z[u] = ldg_stream_if((const T*)a.v + (i + (at < n ? tokens[at] : 0)) * a.v_stride + g * m.d + c, at < n);
+                }
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u)
+                    if (off[u] >= 0 && L.pair >= 0)
+                        ang[u].load(a.rope + ((int64_t)entry * m.page + off[u]) * a.rope_dim, a.rope_dim / 2, L.pair);
+#pragma unroll
+                for (int u = 0; u < kKeys; ++u) {
+                    if (off[u] < 0) continue;
+                    if (L.pair >= 0) ang[u].turn(x[u], y[u], a.interleaved);
+                    T* dst = kc + off[u] * m.token_stride;
+                    *reinterpret_cast<uint4*>(dst + L.a) = x[u];
+                    if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = y[u];
+                    take<T, false>(lo[0], x[u]), take<T, true>(hi[0], x[u]);
+                    take<T, false>(lo[1], y[u]), take<T, true>(hi[1], y[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < kValues; ++u) {
+                    const int32_t at = v0 + u * subs * v_rows;
+                    if (at < n) *reinterpret_cast<uint4*>(vc + offs[at] * m.token_stride + c) = z[u];
                 }
             }
             if (!a.k_bounds) continue;
@@ -437,10 +593,22 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens / (kSms * 4)));
     const int64_t kv_blocks = (a.n_tokens + slice - 1) / slice;
     const int turned = a.rope_dim / 2 / Vec<T>::kN, rows = 32 / (turned + ((m.d - a.rope_dim) / Vec<T>::kN + 1) / 2);
-    int32_t heads = std::min(m.hq, a.n_tokens * m.hq / rows < kSms * 32 ? rows : 4 * rows);
+    const int64_t all = a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv);
+    if (all / rows >= kSms * 32) {  // several times what the SMs hold at once
+        const int32_t heads = 4 * rows, kv_heads = heads / 2;
+        const int64_t units = a.n_tokens * ((a.q ? (m.hq + heads - 1) / heads : 0) + (m.hkv + kv_heads - 1) / kv_heads);
+        const int64_t slices = (a.n_tokens + 31) / 32 * m.hkv;
+        cudaError_t e = launch_overlapped(append_stream_kernel<T>, (units + kWarps - 1) / kWarps, kThreads, 0, st, m, a,
+                                          status, heads);
+        if (e == cudaSuccess && a.k_bounds)
+            e = launch_overlapped(append_bounds_stream_kernel<T>, (slices + kWarps - 1) / kWarps, kThreads, 0, st, m, a,
+                                  status);
+        return note_error(e, "paged append");
+    }
+    const int32_t heads = std::min(m.hq, rows);
     const int64_t q_blocks = a.q ? (a.n_tokens * ((m.hq + heads - 1) / heads) + kWarps - 1) / kWarps : 0;
-    return note_error(launch_overlapped(append_kernel<T>, kv_blocks + q_blocks, kThreads, 0, st, m, a, status, kv_blocks,
-                                        slice, heads),
+    return note_error(launch_overlapped(append_kernel<T>, kv_blocks + q_blocks, kThreads, 0, st, m, a, status,
+                                        kv_blocks, slice, heads),
                       "paged append");
 }
 

@@ -504,14 +504,13 @@ __global__ void __launch_bounds__(kThreads) pick_kernel(PagedMeta m, const T* __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x, b = row / m.hkv, g = row % m.hkv;
     scores += (int64_t)row * m.max_pages;
-    after_previous();
-    // The first scores are asked for before the length is known (a row has max_pages places, written or not).
+    const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
+    after_previous();  // the scores
     constexpr int kAhead = 8;
     uint2 x[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) x[i] = i * kThreads + tid < m.max_pages ? scores[i * kThreads + tid] : make_uint2(0, 0);
+    for (int i = 0; i < kAhead; ++i) x[i] = r.scored && i * kThreads + tid < r.count ? scores[i * kThreads + tid] : make_uint2(0, 0);
     const bool bad = status_bad(status);
-    const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
     const int32_t* trow = table + b * m.table_stride;
     int32_t* out = pages + (int64_t)row * n_select;
     reinterpret_cast<uint4*>(sh.hist)[tid] = make_uint4(0, 0, 0, 0);
