@@ -25,14 +25,13 @@ namespace {
 using sm100::ex2_approx;
 
 constexpr int kTile = 16;          // keys of a unit
-constexpr int kMaxParts = 512;     // most blocks that share the work: counters and partial slots of the workspace
-constexpr size_t kCounterBytes = 4096;
+constexpr int kMaxParts = 192;     // most blocks that share the work: counters and partial slots of the workspace
+constexpr size_t kCounterBytes = 1024;
 constexpr int kSegmentCost = 4;    // units that the beginning of a segment counts
 constexpr int kAlone = 6;          // tiles a warp may have for a block to take a whole segment, without a join of blocks
 constexpr float kLazy = 8.f;       // log2 units a score may exceed the reference before the reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kNone = ~0u;
-constexpr int kMaxDP = 128, kMaxRows = 16;
 
 static_assert(kMaxParts * sizeof(uint32_t) <= kCounterBytes, "counters");
 
@@ -63,9 +62,11 @@ __device__ __forceinline__ uint32_t to_tf32(float x) {
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
-// x = hi + lo with both in tf32, up to 2^-21 |x|. hi is cut, not rounded, so that it stays finite.
+// x = hi + lo with both in tf32, up to 2^-22 |x|. kCut: hi is cut, not rounded, so that it is finite where x is (up to
+// 2^-21 |x| then).
+template <bool kCut>
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
+    hi = kCut ? __float_as_uint(x) & 0xffffe000u : to_tf32(x);
     lo = to_tf32(x - __uint_as_float(hi));
 }
 
@@ -83,6 +84,7 @@ template <int DP, int NT>
 struct Frag<__nv_bfloat16, DP, NT> {
     using T = __nv_bfloat16;
     static constexpr int kOut = DP / 16;  // 16-channel tiles of the output
+    static constexpr int kShared = 0;
     uint4 q[NT][DP / 32];
     uint4 k[DP / 32][2];
     uint4 v[DP / 64][4];
@@ -191,7 +193,8 @@ template <int DP, int NT>
 struct Frag<float, DP, NT> {
     using T = float;
     static constexpr int kOut = DP / 16;
-    float4 q[NT][DP / 16];
+    static constexpr int kShared = NT * DP / 16;  // 16-byte pieces a lane keeps in shared memory: its queries
+    float4* q;                                    // [NT][DP / 16][32]: they would not fit the registers beside K, V and O
     float4 k[DP / 16][2];
     float4 v[DP / 32][4];
     float o[NT][kOut][4];
@@ -207,9 +210,10 @@ struct Frag<float, DP, NT> {
 #pragma unroll
             for (int j = 0; j < DP / 16; ++j) {
                 const int c = 16 * j + 4 * t;
-                q[n][j] = n * 8 + g < rows && c < d
-                              ? __ldg(reinterpret_cast<const float4*>(base + (int64_t)(n * 8 + g) * d + c))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                q[(n * DP / 16 + j) * 32 + lane] =
+                    n * 8 + g < rows && c < d
+                        ? __ldg(reinterpret_cast<const float4*>(base + (int64_t)(n * 8 + g) * d + c))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
             }
     }
     __device__ __forceinline__ void load_k(const T* kc, const TileRows& r, int d, int lane) {
@@ -238,23 +242,23 @@ struct Frag<float, DP, NT> {
             }
         }
     }
-    // acc += a b over 8 channels, a [16 x 8] as four values a lane. An infinite value has no halves: kInf keeps it to
-    // the product of the high ones.
-    template <bool kInf = false>
+    // acc += a b over 8 channels, a [16 x 8] as four values a lane. kCut: a may be as large as the type goes. kInf: a or b
+    // may be infinite and have no halves then; only the product of the high ones sees it.
+    template <bool kCut, bool kInf>
     static __device__ __forceinline__ void product(float (&acc)[NT][4], const float (&a)[4], const float (&b0)[NT],
                                                    const float (&b1)[NT]) {
         uint32_t hi[4], lo[4], fin[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            split_tf32(a[i], hi[i], lo[i]);
+            split_tf32<kCut>(a[i], hi[i], lo[i]);
             fin[i] = hi[i];
             if (kInf && !isfinite(a[i])) lo[i] = fin[i] = 0;
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             uint32_t h0, l0, h1, l1;
-            split_tf32(b0[n], h0, l0);
-            split_tf32(b1[n], h1, l1);
+            split_tf32<kInf>(b0[n], h0, l0);
+            split_tf32<kInf>(b1[n], h1, l1);
             uint32_t f0 = h0, f1 = h1;
             if (kInf && !isfinite(b0[n])) l0 = f0 = 0;
             if (kInf && !isfinite(b1[n])) l1 = f1 = 0;
@@ -270,20 +274,21 @@ struct Frag<float, DP, NT> {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) nan |= s[n][i] != s[n][i];
-        if (__any_sync(0xffffffffu, nan)) sums<true>(s);  // infinite keys or queries
+        if (__any_sync(0xffffffffu, nan)) sums<true>(s);  // infinite keys or queries, or near the type's end
     }
     template <bool kInf>
     __device__ __forceinline__ void sums(float (&s)[NT][4]) const {
         float a[2][NT][4] = {};
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j) {
-            float b0[NT], b1[NT];
+            float b[4][NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) b0[n] = q[n][j].x, b1[n] = q[n][j].y;
-            product<kInf>(a[0], {k[j][0].x, k[j][1].x, k[j][0].y, k[j][1].y}, b0, b1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b0[n] = q[n][j].z, b1[n] = q[n][j].w;
-            product<kInf>(a[1], {k[j][0].z, k[j][1].z, k[j][0].w, k[j][1].w}, b0, b1);
+            for (int n = 0; n < NT; ++n) {
+                const float4 y = q[(n * DP / 16 + j) * 32 + (threadIdx.x & 31)];
+                b[0][n] = y.x, b[1][n] = y.y, b[2][n] = y.z, b[3][n] = y.w;
+            }
+            product<kInf, kInf>(a[0], {k[j][0].x, k[j][1].x, k[j][0].y, k[j][1].y}, b[0], b[1]);
+            product<kInf, kInf>(a[1], {k[j][0].z, k[j][1].z, k[j][0].w, k[j][1].w}, b[2], b[3]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -315,9 +320,9 @@ struct Frag<float, DP, NT> {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[n][i] = o[n][2 * c0 + w][i];
                     if (w == 0)
-                        product(acc, {y.x, y.y, z.x, z.y}, b0, b1);
+                        product<true, false>(acc, {y.x, y.y, z.x, z.y}, b0, b1);
                     else
-                        product(acc, {y.z, y.w, z.z, z.w}, b0, b1);
+                        product<true, false>(acc, {y.z, y.w, z.z, z.w}, b0, b1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     __shared__ float scale_of[2 * W][R];   // 1 / sum of a finished row
     __shared__ Group group[2 * W];
     __shared__ Side side[2];
-    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + sizeof(P) * W * 2);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + sizeof(P) * W * 2 + Frag<T, DP, NT>::kShared * 512 * W);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row_groups = (m.group + R - 1) / R;
 
@@ -499,6 +504,8 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     const uint32_t w_lo = c_lo + warp * each + min((uint32_t)warp, more), w_hi = w_lo + each + ((uint32_t)warp < more);
 
     Frag<T, DP, NT> f;
+    if constexpr (Frag<T, DP, NT>::kShared > 0)
+        f.q = reinterpret_cast<float4*>(smem + sizeof(P) * W * 2) + warp * (Frag<T, DP, NT>::kShared * 32);
     const float to_log2 = m.scale * kLog2e;
     for (uint32_t u = skip ? w_hi : w_lo; u < w_hi;) {
         const Segment sg = segment_at(L, u);
@@ -827,10 +834,11 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const size_t smem = sizeof(P) * W * 2 + sizeof(int32_t) * std::max(m.n_seqs + 1, W * 36);
+    constexpr size_t kFixed = sizeof(P) * W * 2 + Frag<T, DP, NT>::kShared * 512 * W;
+    const size_t smem = kFixed + sizeof(int32_t) * std::max(m.n_seqs + 1, W * 36);
     auto kern = decode_kernel<T, DP, NT, W>;
     static SmemGrants granted;
-    e = allow_smem((const void*)kern, sizeof(P) * W * 2 + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), granted);
+    e = allow_smem((const void*)kern, kFixed + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), granted);
     if (e != cudaSuccess) return e;
     const int grid = std::min(sms, kMaxParts);
     return note_error(launch_overlapped(kern, grid, W * 32, smem, st, m, (const T*)q, q_stride, (const T*)k_cache,
@@ -841,8 +849,9 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
 
 }  // namespace
 
-size_t paged_decode_workspace(const PagedMeta&) {
-    return kCounterBytes + sizeof(Partial<kMaxDP, kMaxRows>) * kMaxParts * 2;
+size_t paged_decode_workspace(const PagedMeta& m) {
+    const size_t rows = m.group > 8 && m.dtype == SPLITKV_BF16 ? 16 : 8, channels = m.d <= 64 ? 64 : 128;
+    return kCounterBytes + rows * (channels + 2) * sizeof(float) * kMaxParts * 2;
 }
 
 cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,

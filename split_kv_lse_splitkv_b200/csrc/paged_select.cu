@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace splitkv {
 namespace {
@@ -58,6 +59,8 @@ struct Chunk<__nv_bfloat16> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+    // The larger sizes, channel by channel, as the type's bits (infinities above all numbers, NaN above them).
+    static __device__ __forceinline__ uint32_t larger(uint32_t size, uint32_t x) { return __vmaxu2(size, x & 0x7fff7fffu); }
 };
 template <>
 struct Chunk<float> {
@@ -65,6 +68,7 @@ struct Chunk<float> {
     static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[4]) {
         f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
     }
+    static __device__ __forceinline__ uint32_t larger(uint32_t size, uint32_t x) { return max(size, x & 0x7fffffffu); }
 };
 
 // How many pages of a sequence have to be scored, and which are taken without: pages < lead and >= tail.
@@ -83,7 +87,9 @@ __device__ __forceinline__ Row row_of(const PagedMeta& m, int32_t len, int32_t n
     return r;
 }
 
-// ---- first kernel: {key of the float32 score (0: not ranked), bound on the sum of its terms' sizes} of every page.
+// ---- first kernel: {key of the float32 score (0: not ranked), bound on the sums of terms' sizes} of every page. The
+// bound stands with the last page of a warp's share, for all of the share: the sum over the channels of the coefficient's
+// size times the largest size among the pages (2 instructions a pair of channels; a sum per page would take 4).
 // LP lanes hold the 2d channels of one page, NC chunks of 16 bytes each.
 template <typename T, int LP, int NC>
 __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
@@ -191,31 +197,33 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
                     for (int j = 0; j < kN; ++j) c[k][j] += (e < m.d) != (f[j] > 0.f) ? f[j] : 0.f;  // (NaN: into one of them)
                 }
             }
-        uint4 x[kV][NC], ahead[kV][NC];
+        uint4 x[kV][NC], ahead[kV][NC], sizes[NC] = {};
         load(mine, x);
         auto round = [&](const uint4 (&x)[kV][NC]) {
-            float s[kV], size = 0.f;
+            float s[kV];
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                float terms = 0.f;
-                s[v] = 0.f;
+                uint64_t sum = 0;  // of the even and of the odd channels
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     float f[kN];
                     Chunk<T>::unpack(x[v][k], f);
 #pragma unroll
-                    for (int j = 0; j < kN; ++j) {
-                        const float y = f[j] * c[k][j];
-                        s[v] += y, terms += fabsf(y);
-                    }
+                    for (int j = 0; j < kN; j += 2)
+                        sum = sm100::f2_fma(sm100::f2_pack(f[j], f[j + 1]), sm100::f2_pack(c[k][j], c[k][j + 1]), sum);
+                    sizes[k].x = Chunk<T>::larger(sizes[k].x, x[v][k].x);
+                    sizes[k].y = Chunk<T>::larger(sizes[k].y, x[v][k].y);
+                    sizes[k].z = Chunk<T>::larger(sizes[k].z, x[v][k].z);
+                    sizes[k].w = Chunk<T>::larger(sizes[k].w, x[v][k].w);
                 }
-                size = max_nan(size, terms);
+                float even, odd;
+                sm100::f2_unpack(sum, even, odd);
+                s[v] = even + odd;
             }
             // Sums over the LP lanes; halving the values at each step while there are several: lane `sub` ends up
             // with the sum of value (sub * values / LP), the lanes of a value side by side.
 #pragma unroll
             for (int step = LP / 2, have = kV; step; step >>= 1) {
-                size += __shfl_xor_sync(0xffffffffu, size, step);
                 if (have > 1) {
                     have >>= 1;
 #pragma unroll
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
             const int32_t page = __shfl_sync(0xffffffffu, mine, (v * kPer + at) & 31);
             if (sub % (LP / kV) == 0 && at_p < p_end) {
                 const bool kept = at_p < keep_first || at_p >= count - keep_last;
-                out[at_p] = make_uint2(kept || page < 0 ? 0 : score_key(s[0]), __float_as_uint(size));
+                out[at_p] = make_uint2(kept || page < 0 ? 0 : score_key(s[0]), 0);
             }
             mine = next;
             p += kStep;
@@ -249,6 +257,20 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
             next = after;
             if (p >= p_end) break;
         }
+        float size = 0.f;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            float f[kN];
+            Chunk<T>::unpack(sizes[k], f);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) size = fmaf(f[j], fabsf(c[k][j]), size);
+        }
+#pragma unroll
+        for (int step = LP / 2; step; step >>= 1) size += __shfl_xor_sync(0xffffffffu, size, step);
+#pragma unroll
+        for (int step = 16; step >= LP; step >>= 1) size = max_nan(size, __shfl_xor_sync(0xffffffffu, size, step));
+        __syncwarp();  // after the key beside it
+        if (lane == 0) out[p_end - 1].y = __float_as_uint(size);
     }
 }
 
@@ -488,8 +510,8 @@ __device__ __noinline__ void pick_wide(const PagedMeta& m, const T* q, const T* 
     write_pages(wide, sh, r, take, lo, hi, ties, out, n_select);
 }
 
-// A float32 score's error over the sum of its terms' sizes: the coefficients' sums (G - 1), products (1), at most 8 terms
-// in a lane's sum and 5 sums of lanes (13), each rounding 2^-24 of something no larger; the sizes' own sums as much.
+// A float32 score's error over the sum of its terms' sizes: the coefficients' sums (G - 1), at most 8 terms in a lane's sum,
+// 1 sum of two and 5 of lanes (14), each rounding 2^-24 of something no larger; the sizes' own sums as much.
 __device__ __forceinline__ float error_of(const PagedMeta& m) { return (32 + 2 * m.group) * 0x1p-24f; }
 
 // One block per (sequence, kv head).

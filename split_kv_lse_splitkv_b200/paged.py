@@ -14,7 +14,7 @@ import torch
 from . import binding as B
 from .binding import EINVAL, SplitKVError
 
-_COUNTERS = 4096  # bytes at the head of the workspace that have to be zero before its first use
+_COUNTERS = 1024  # bytes at the head of the workspace that have to be zero before its first use
 _MOST = (1 << 31) - 1
 _I32, _F32 = torch.int32, torch.float32
 _append, _select, _decode = B._lib.splitkv_paged_append, B._lib.splitkv_paged_select, B._lib.splitkv_paged_decode
@@ -91,16 +91,19 @@ class PagedKV:
         self._ws_bytes = B._lib.splitkv_paged_workspace_size(whole, self.max_seqs)
         if self._ws_bytes == 0:  # let the library say what is wrong with the description
             raise SplitKVError(_decode(whole, self.max_seqs, *[0] * 14), "PagedKV")
-        self.status = torch.zeros(1, dtype=_I32, device=self.device)
+        self._lock = threading.Lock()
+        self._ws = self._stream = None
+        if self._index is None:
+            self.status = torch.zeros(1, dtype=_I32, device=self.device)
+        else:  # the status word and the scratch, whose counters start at zero
+            self._ws = torch.empty(16 + self._ws_bytes, dtype=torch.uint8, device=self.device)
+            self._ws[:16 + _COUNTERS].zero_()
+            self.status = self._ws[:4].view(_I32)
+            self._ws_at = self._ws.data_ptr() + 16
+            self._stream = torch.cuda.current_stream(self.device)
         # The object's own tensors, which it keeps.
         self._k_at, self._v_at, self._status_at = k_cache.data_ptr(), v_cache.data_ptr(), self.status.data_ptr()
         self._bounds_at = None if k_bounds is None else k_bounds.data_ptr()
-        self._lock = threading.Lock()
-        self._ws = self._stream = None
-        if self._index is not None:
-            self._ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
-            self._ws_at = self._ws.data_ptr()
-            self._stream = torch.cuda.current_stream(self.device)
 
     # -- marshalling. These calls are made once per layer and token: checks are plain comparisons, texts are made only where
     # one fails, and the library is called with integers.
