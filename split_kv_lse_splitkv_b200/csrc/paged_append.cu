@@ -275,41 +275,104 @@ __device__ __forceinline__ void check_order(const AppendArgs& a, int64_t i, int3
     if (before > seq || (before == seq && before_pos >= pos)) raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
 }
 
-// Many tokens: every token's rows by themselves; a warp has `heads` heads of its queries, or half as many of its keys and
-// values. The bounds of the keys follow in a launch of their own, from L2. (A page's rows and bounds in one block, as
-// below, keep too few loads in flight to fill the GPU: 35k tokens took 52 us for keys and values alone, against
-// 23 us for their bytes.)
+// Many tokens: rows by themselves. A unit is `most` rows: that many heads of one token, or all heads of several tokens
+// where they are few. A warp has a unit of queries, or one of keys and the same one of values. The bounds of the keys
+// follow in a launch of their own, from L2. (A page's rows and bounds in one block, as below, keep too few loads in
+// flight to fill the GPU: 35k tokens took 52 us for keys and values alone, against 23 us for their bytes.)
+struct Units {
+    int32_t heads, tokens;  // of a unit
+    int32_t per_token;      // units that a token's heads take
+    __host__ __device__ Units(int32_t all, int32_t most)
+        : heads(all < most ? all : most), tokens(most / heads), per_token((all + heads - 1) / heads) {}
+    __host__ __device__ int64_t of(int64_t n) const { return (n + tokens - 1) / tokens * per_token; }
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status,
-                                                                    int32_t heads) {
+__global__ void __launch_bounds__(kThreads, 4) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     after_previous();
     if (status_bad(status)) return;
     const int lane = threadIdx.x & 31;
-    const int32_t q_units = a.q ? (m.hq + heads - 1) / heads : 0, kv_heads = heads / 2;
-    const int32_t per_token = q_units + (m.hkv + kv_heads - 1) / kv_heads;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), i = unit / per_token;
-    if (i >= a.n_tokens) return;
-    const int32_t j = (int32_t)(unit - i * per_token);
-    if (j < q_units) {
-        append_queries<T, 2>(m, a, i, j * heads, min((j + 1) * heads, m.hq), lane);
+    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    const Units Q(m.hq, 4 * L.rows), KV(m.hkv, 2 * L.rows);
+    int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t q_units = a.q ? Q.of(a.n_tokens) : 0;
+    const bool queries = unit < q_units;
+    const Units U = queries ? Q : KV;
+    if (!queries) unit -= q_units;
+    const int64_t i0 = unit / U.per_token * U.tokens;
+    const int32_t h0 = (int32_t)(unit % U.per_token) * U.heads;
+    // Row x of the unit: token i0 + x / heads, head h0 + x % heads; a lane has rows L.row + k * L.rows.
+    auto row = [&](int k, int64_t& i, int32_t& h) {
+        const int32_t x = L.row + k * L.rows, t = U.tokens == 1 ? x >= U.heads : x / U.heads;
+        i = i0 + t, h = h0 + x - t * U.heads;
+        return L.row < L.rows && t < U.tokens && i < a.n_tokens && h < (queries ? m.hq : m.hkv);
+    };
+    Angles<T> ang;
+    int64_t i[2];
+    int32_t h[2];
+    bool in[2];
+    uint4 x[2], y[2];
+    if (queries) {
+        int64_t now = -1;  // the token whose angles are at hand
+        bool turn = false;
+        for (int step = 0; step < 4; step += 2) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                in[k] = row(step + k, i[k], h[k]);
+                const T* src = (const T*)a.q + i[k] * a.q_stride + (int64_t)h[k] * m.d;
+                x[k] = ldg_stream_if(src + L.a, in[k]);
+                y[k] = ldg_stream_if(src + L.b, in[k] && L.b >= 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (!in[k]) continue;
+                if (i[k] != now) {
+                    now = i[k];
+                    const int32_t seq = __ldg(a.token_seq + now), pos = __ldg(a.token_pos + now);
+                    // A token that is out of range is reported with its keys; its queries pass as they are.
+                    turn = L.pair >= 0 && seq >= 0 && pos >= 0 && pos < a.rope_len;
+                    if (turn) ang.load(a.rope + (int64_t)pos * a.rope_dim, a.rope_dim / 2, L.pair);
+                }
+                if (turn) ang.turn(x[k], y[k], a.interleaved);
+                T* dst = (T*)a.q_out + (i[k] * m.hq + h[k]) * m.d;
+                *reinterpret_cast<uint4*>(dst + L.a) = x[k];
+                if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = y[k];
+            }
+        }
         return;
     }
-    const int32_t h0 = (j - q_units) * kv_heads, h1 = min(h0 + kv_heads, m.hkv);
-    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
-    Rows<T, 2> k, v;
-    k.load(m, L, (const T*)a.k + i * a.k_stride, h0 + L.row, h1);
-    v.load(m, L, (const T*)a.v + i * a.v_stride, h0 + L.row, h1);
-    const TokenPlace t = token_place(m, a, i, status);
-    if (j == q_units && lane == 0 && t.seq >= 0) {
-        int32_t before, before_pos;
-        check_order(a, i, t.seq, t.pos, status, before, before_pos);
+    uint4 z[2], w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        in[k] = row(k, i[k], h[k]);
+        const T* src = (const T*)a.k + i[k] * a.k_stride + (int64_t)h[k] * m.d;
+        x[k] = ldg_stream_if(src + L.a, in[k]);
+        y[k] = ldg_stream_if(src + L.b, in[k] && L.b >= 0);
+        src = (const T*)a.v + i[k] * a.v_stride + (int64_t)h[k] * m.d;
+        z[k] = ldg_stream_if(src + L.a, in[k]);
+        w[k] = ldg_stream_if(src + L.b, in[k] && L.b >= 0);
     }
-    if (t.page < 0) return;
-    Angles<T> ang;
-    if (L.pair >= 0) ang.load(a.rope + (int64_t)t.pos * a.rope_dim, a.rope_dim / 2, L.pair);
-    const int64_t at = paged_row(m, t.page, 0, t.pos & (m.page - 1));
-    k.store(a, L, (T*)a.k_cache + at, m.head_stride, h0 + L.row, h1, L.pair >= 0 ? &ang : nullptr);
-    v.store(a, L, (T*)a.v_cache + at, m.head_stride, h0 + L.row, h1, nullptr);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (!in[k]) continue;
+        const TokenPlace t = token_place(m, a, i[k], status);
+        if (h[k] == 0 && L.a == 0 && t.seq >= 0) {
+            int32_t before, before_pos;
+            check_order(a, i[k], t.seq, t.pos, status, before, before_pos);
+        }
+        if (t.page < 0) continue;
+        if (L.pair >= 0) {
+            ang.load(a.rope + (int64_t)t.pos * a.rope_dim, a.rope_dim / 2, L.pair);
+            ang.turn(x[k], y[k], a.interleaved);
+        }
+        const int64_t at = paged_row(m, t.page, h[k], t.pos & (m.page - 1));
+        T* dst = (T*)a.k_cache + at;
+        *reinterpret_cast<uint4*>(dst + L.a) = x[k];
+        if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = y[k];
+        dst = (T*)a.v_cache + at;
+        *reinterpret_cast<uint4*>(dst + L.a) = z[k];
+        if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = w[k];
+    }
 }
 
 // Which of the 32 tokens from i0 on (a lane each) are the first of the call in their page. `report`: say what is wrong
@@ -595,11 +658,10 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     const int turned = a.rope_dim / 2 / Vec<T>::kN, rows = 32 / (turned + ((m.d - a.rope_dim) / Vec<T>::kN + 1) / 2);
     const int64_t all = a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv);
     if (all / rows >= kSms * 32) {  // several times what the SMs hold at once
-        const int32_t heads = 4 * rows, kv_heads = heads / 2;
-        const int64_t units = a.n_tokens * ((a.q ? (m.hq + heads - 1) / heads : 0) + (m.hkv + kv_heads - 1) / kv_heads);
+        const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
         const int64_t slices = (a.n_tokens + 31) / 32 * m.hkv;
         cudaError_t e = launch_overlapped(append_stream_kernel<T>, (units + kWarps - 1) / kWarps, kThreads, 0, st, m, a,
-                                          status, heads);
+                                          status);
         if (e == cudaSuccess && a.k_bounds)
             e = launch_overlapped(append_bounds_stream_kernel<T>, (slices + kWarps - 1) / kWarps, kThreads, 0, st, m, a,
                                   status);
