@@ -24,7 +24,9 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits;
-constexpr int kLoads = 8;         // loads of bounds a lane has in flight, and again as many for the round after
+constexpr int kLoads = 8;         // copies of 16 bytes of bounds a lane makes in a round
+constexpr int kStages = 3;        // rounds in flight and in use
+constexpr int kRing = kWarps * kStages * kLoads * 32;  // 16-byte pieces: 192 KB
 constexpr int kInShared = 16384;  // scores that the second kernel keeps in shared memory; longer rows stay in L2
 constexpr int kCands = 512;       // pages that are ranked one by one
 constexpr int kWords = 512, kSpan = kWords * 32;
@@ -101,9 +103,10 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
     constexpr int kN = Chunk<T>::kN, kPer = 32 / LP;    // pages a warp reads with one load a lane
     constexpr int kV = kLoads / NC, kStep = kV * kPer;  // pages of a lane's round, of a warp's
     static_assert(kStep <= 32 && LP >= kV, "one table entry, one result a lane");
-    extern __shared__ int32_t prefix_all[];  // pages to score of the sequences before b
-    int32_t* prefix = prefix_all;
+    extern __shared__ uint4 smem[];
+    int32_t* prefix = reinterpret_cast<int32_t*>(smem + kRing);  // pages to score of the sequences before b
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint4* const ring = smem + warp * (kStages * kLoads * 32) + lane;
     after_previous();
     const bool bad = status_bad(status);
     auto pages_of = [&](int b) {
@@ -166,19 +169,28 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
         uint2* out = scores + ((int64_t)b * m.hkv + g) * m.max_pages;
 
         auto entry = [&](int32_t p) { return lane < kStep && p + lane < p_end ? paged_page(m, trow, p + lane, status) : -1; };
-        auto load = [&](int32_t mine, uint4 (&x)[kV][NC]) {
+        // Asynchronous copies into a ring of rounds in shared memory: two rounds are on their way while one is summed. (Loads
+        // into registers one round ahead left the warps waiting for most of the time: 12 bytes a clock and SM.) A lane
+        // reads back what it copied itself, so nothing has to be synchronised.
+        auto fetch = [&](int32_t mine, int stage) {
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 const int32_t page = __shfl_sync(0xffffffffu, mine, v * kPer + at);
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
                     const int e = (k * LP + sub) * kN;
-                    x[v][k] = ldg_stream_if(head + page * page_step + e, page >= 0 && e < 2 * m.d);
+                    const bool in = page >= 0 && e < 2 * m.d;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     sm100::smem_u32(ring + (stage * kLoads + v * NC + k) * 32)),
+                                 "l"(in ? head + page * page_step + e : head), "r"(in ? 16 : 0)
+                                 : "memory");
                 }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // The next round's bounds are on their way during a round, the table's entries one round more.
-        int32_t mine = entry(p), next = entry(p + kStep);
+        int32_t ids[kStages + 1];  // table entries of this round and the next ones
+#pragma unroll
+        for (int r = 0; r <= kStages; ++r) ids[r] = entry(p + r * kStep);
         float c[NC][kN] = {};
         for (int h0 = 0; h0 < m.group; h0 += 4)
 #pragma unroll
@@ -197,9 +209,18 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
                     for (int j = 0; j < kN; ++j) c[k][j] += (e < m.d) != (f[j] > 0.f) ? f[j] : 0.f;  // (NaN: into one of them)
                 }
             }
-        uint4 x[kV][NC], ahead[kV][NC], sizes[NC] = {};
-        load(mine, x);
-        auto round = [&](const uint4 (&x)[kV][NC]) {
+#pragma unroll
+        for (int r = 0; r < kStages - 1; ++r) fetch(ids[r], r);
+        uint4 sizes[NC] = {};
+        for (int stage = 0;; stage = stage + 1 < kStages ? stage + 1 : 0) {
+            const int32_t after = entry(p + (kStages + 1) * kStep);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            uint4 x[kV][NC];
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+#pragma unroll
+                for (int k = 0; k < NC; ++k) x[v][k] = ring[(stage * kLoads + v * NC + k) * 32];
+            fetch(ids[kStages - 1], stage == 0 ? kStages - 1 : stage - 1);
             float s[kV];
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
@@ -237,26 +258,17 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* _
                 }
             }
             const int v = sub / (LP / kV), at_p = p + v * kPer + at;
-            const int32_t page = __shfl_sync(0xffffffffu, mine, (v * kPer + at) & 31);
+            const int32_t page = __shfl_sync(0xffffffffu, ids[0], (v * kPer + at) & 31);
             if (sub % (LP / kV) == 0 && at_p < p_end) {
                 const bool kept = at_p < keep_first || at_p >= count - keep_last;
                 out[at_p] = make_uint2(kept || page < 0 ? 0 : score_key(s[0]), 0);
             }
-            mine = next;
-            p += kStep;
-        };
-        for (;;) {
-            int32_t after = entry(p + 2 * kStep);
-            load(next, ahead);
-            round(x);
-            next = after;
-            if (p >= p_end) break;
-            after = entry(p + 2 * kStep);
-            load(next, x);
-            round(ahead);
-            next = after;
-            if (p >= p_end) break;
+            if ((p += kStep) >= p_end) break;
+#pragma unroll
+            for (int r = 0; r < kStages; ++r) ids[r] = ids[r + 1];
+            ids[kStages] = after;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");  // (what runs past the share copies nothing)
         float size = 0.f;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
@@ -626,8 +638,12 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     static SmemGrants granted;
     e = allow_smem((const void*)pick, sizeof(uint32_t) * kInShared, granted);
     if (e != cudaSuccess) return e;
-    const size_t lens = sizeof(int32_t) * std::max(m.n_seqs + 1, kWarps * 36);
-    e = launch_overlapped(score_kernel<T, LP, NC>, sms, kThreads, lens, st, m, (const T*)q, q_stride, (const T*)k_bounds,
+    auto score = score_kernel<T, LP, NC>;
+    static SmemGrants score_granted;
+    e = allow_smem((const void*)score, sizeof(uint4) * kRing + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), score_granted);
+    if (e != cudaSuccess) return e;
+    const size_t lens = sizeof(uint4) * kRing + sizeof(int32_t) * std::max(m.n_seqs + 1, kWarps * 36);
+    e = launch_overlapped(score, sms, kThreads, lens, st, m, (const T*)q, q_stride, (const T*)k_bounds,
                           table, seq_len, n_select, keep_first, keep_last, (uint2*)ws, status);
     if (e == cudaSuccess)
         e = launch_overlapped(pick, m.n_seqs * m.hkv, kThreads, sizeof(uint32_t) * std::min(m.max_pages, kInShared), st, m,
