@@ -353,6 +353,49 @@ def test_append_padding_and_options():
     run_append([7] * 300, [1] * 300, 8, 2, 64, 16, F32, 64, False)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hq,hkv,d,rot,interleaved", [(32, 4, 128, 128, False), (3, 1, 128, 64, True), (40, 10, 64, 64, False),
+                                                      (1, 1, 16, 16, False), (6, 2, 80, 0, False), (8, 8, 112, 112, True)])
+@pytest.mark.parametrize("page", [4, 64])
+def test_append_many_tokens(dtype, hq, hkv, d, rot, interleaved, page):
+    # Enough rows that they stream one by one, with their bounds in a second launch: sequences that begin and end inside
+    # pages, padding inside and behind them.
+    n = 148 * 32 * (32 // max(1, (d * (2 if dtype == BF else 4) + 31) // 32)) // (hq + 2 * hkv) + 100
+    lens, new = [n // 2 + 3, 5, n // 2, 70], [n // 2 - 9, 5, n // 2, 1]
+    run_append(lens, new, hq, hkv, d, page, dtype, rot, interleaved, padding=(0, 7, 40, 41, 300), seed=d)
+
+
+def test_append_many_tokens_orders_and_options():
+    run_append([3000, 2000], [2500, 2000], 8, 2, 128, 32, BF, 128, False, order="positions")
+    run_append([3000, 2000], [2500, 2000], 8, 2, 128, 32, F32, 128, True, order="gaps")
+    run_append([9000], [9000], 8, 2, 128, 1024, BF, 128, False, with_q=False)
+    run_append([9000], [8990], 8, 2, 128, 1, BF, 128, False, with_q=False)
+    run_append([9000], [8990], 8, 2, 128, 16, BF, 64, False, bounds=False)
+
+
+@pytest.mark.parametrize("what,bit", [("order", B.DEV_TOKEN_ORDER), ("seq", B.DEV_BAD_TOKEN), ("pos", B.DEV_BAD_TOKEN),
+                                      ("page", B.DEV_BAD_PAGE)])
+def test_append_many_tokens_bad_ones_raise_the_status(what, bit):
+    n = 9000
+    c = Case([n], 8, 2, 128, 16)
+    kb = torch.zeros(c.k.shape[0], 2, 2, 128, dtype=BF, device="cuda")
+    kv = PagedKV(8, 2, 128, 16, max_seqs=1, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    table = c.table.clone()
+    if what == "order":
+        pos[5000] = 4999
+    elif what == "seq":
+        seq[5000:] = 1
+    elif what == "pos":
+        pos[n - 1] = table.shape[1] * 16
+    else:
+        table[0, 300] = c.k.shape[0]
+    x = torch.zeros(n, 2, 128, dtype=BF, device="cuda")
+    kv.append(x, x, table, seq, pos, q=torch.zeros(n, 8, 128, dtype=BF, device="cuda"), rope=rope_table(n + 100, 128))
+    assert kv.status_value() == bit
+
+
 def test_append_follows_a_sequence_that_was_cut_back():
     # Ten positions written, five of them given up, one written anew: the bounds are those of the six that count.
     c = run_append([10], [10], 4, 2, 64, 16, BF, 64, False)
