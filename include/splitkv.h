@@ -355,8 +355,11 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
  *                     times with the lengths that each of them sees.
  *   q, o              [n_seqs, Hq, d]; q's tokens are q_stride elements apart (a slice of a fused
  *                     projection), each token's heads dense; o and lse [n_seqs, Hq] are dense.
- * Pointers are 16-byte aligned and every stride a multiple of 16 bytes. Sums, maxima and partial
- * results are float32; scores that choose pages are float64, so that no rounding decides a choice.
+ * Pointers are 16-byte aligned and every stride a multiple of 16 bytes (k_cache, v_cache, k_bounds, q, k,
+ * v, o, rope and workspaces; lists and tables of int32 need their own alignment only). Sums, maxima and
+ * partial results are float32; the choice of pages is that of float64 scores, so that no rounding decides it.
+ * The kernels are launched so that they may be placed on the SMs while the kernel before them in the
+ * stream drains; they touch memory only once it has completed.
  * Lengths, tables and token lists are device data, read by the kernels only: a call captured into a
  * CUDA graph follows their values at each replay. What only the device can see (lengths, pages and
  * tokens out of range) is ORed into status_d; the results of that call are then unspecified, but
@@ -395,7 +398,7 @@ size_t splitkv_paged_workspace_size(const splitkv_paged *paged, int32_t n_seqs);
  * no position is given twice.
  *   k, v   [n_tokens, Hkv, d], tokens k_stride and v_stride elements apart, each token's heads dense.
  *   q      [n_tokens, Hq, d] (q_stride) or NULL: rotated into q_out [n_tokens, Hq, d] (dense, apart from
- *          q). A padding token's queries are copied as they are.
+ *          q, k and v). A padding token's queries are copied as they are.
  *   rope   float32 [rope_len, rope_dim], or NULL (no rotation; rope_dim = 0): row p holds rope_dim/2 cosines
  *          and then rope_dim/2 sines for position p. Channel pairs (i, i + rope_dim/2), or (2i, 2i+1) with
  *          interleaved != 0, turn by angle i: (x c - y s, y c + x s), in float32, rounded once; channels

@@ -519,13 +519,14 @@ SPLITKV_API int splitkv_paged_append(const splitkv_paged* paged, int32_t n_seqs,
     if (q && (!rows_ok(m, q, n_tokens, q_stride, m.hq) || !q_out || !aligned16(q_out))) return SPLITKV_EINVAL;
     if (!page_table_d || !token_seq_d || !token_pos_d || !k_cache || !v_cache) return SPLITKV_EINVAL;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_bounds) || !aligned16(rope)) return SPLITKV_EINVAL;
-    if (q) {  // q_out is written while other blocks still read q
-        const int64_t e = m.dtype == SPLITKV_BF16 ? 2 : 4, row = (int64_t)m.hq * m.d * e;
-        const char *x = (const char*)q, *y = (const char*)q_out;
-        if (x < y + n_tokens * row && y < x + (n_tokens - 1) * q_stride * e + row) {
-            // A fused projection's rows may enclose the output's only if they are apart in memory: refuse any overlap.
-            return SPLITKV_EINVAL;
-        }
+    if (q) {  // q_out is written while other blocks still read q, k and v: refuse any overlap of their ranges
+        const int64_t e = m.dtype == SPLITKV_BF16 ? 2 : 4;
+        const char* y = (const char*)q_out;
+        auto over = [&](const void* x, int64_t stride, int32_t heads) {
+            const int64_t bytes = ((n_tokens - 1) * (n_tokens > 1 ? stride : 0) + (int64_t)heads * m.d) * e;
+            return (const char*)x < y + n_tokens * m.hq * m.d * e && y < (const char*)x + bytes;
+        };
+        if (over(q, q_stride, m.hq) || over(k, k_stride, m.hkv) || over(v, v_stride, m.hkv)) return SPLITKV_EINVAL;
     }
     const AppendArgs a{n_tokens, q,           k,          v,           q_stride,    k_stride, v_stride,
                        rope,     rope_dim,    interleaved, rope_len,   page_table_d, token_seq_d, token_pos_d,

@@ -50,7 +50,7 @@ class PagedKV:
     :meth:`select` only (``bounds=True`` allocates it).
 
     Every call takes a page table (int32 [n_seqs, up to max_pages]: row b lists the pages of sequence b) and is
-    enqueued on the current stream (``stream=``: on that one); none synchronizes. Lengths, tables and token lists
+    enqueued on the current stream (``stream=``: on that one); none synchronizes (making the object does). Lengths, tables and token lists
     are read on the device, so a call captured into a CUDA graph follows their values at each replay. The object's
     scratch is shared by its decode calls: on a change of stream the new one waits for the old one, and a captured
     call has scratch of its own. Errors that only the device sees collect in :attr:`status`.
@@ -95,12 +95,15 @@ class PagedKV:
         self._ws = self._stream = None
         if self._index is None:
             self.status = torch.zeros(1, dtype=_I32, device=self.device)
-        else:  # the status word and the scratch, whose counters start at zero
+        else:  # the status word and the scratch, whose counters start at zero: before any stream's first call
+            if torch.cuda.is_current_stream_capturing():
+                raise SplitKVError(EINVAL, "PagedKV: made during a stream capture")
             self._ws = torch.empty(16 + self._ws_bytes, dtype=torch.uint8, device=self.device)
             self._ws[:16 + _COUNTERS].zero_()
             self.status = self._ws[:4].view(_I32)
             self._ws_at = self._ws.data_ptr() + 16
             self._stream = torch.cuda.current_stream(self.device)
+            self._stream.synchronize()
         # The object's own tensors, which it keeps.
         self._k_at, self._v_at, self._status_at = k_cache.data_ptr(), v_cache.data_ptr(), self.status.data_ptr()
         self._bounds_at = None if k_bounds is None else k_bounds.data_ptr()

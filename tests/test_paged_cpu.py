@@ -167,6 +167,7 @@ def test_append_refusals():
                      (dict(rope_dim=63), B.EINVAL), (dict(rope_dim=66), B.EINVAL), (dict(rope_len=0), B.EINVAL),
                      (dict(rope=None), B.EINVAL),                            # rope_dim without a table
                      (dict(q_out=f), B.EINVAL), (dict(q_out=f[128:]), B.EINVAL),  # over q itself
+                     (dict(k=far[64:]), B.EINVAL), (dict(v=far[1024:]), B.EINVAL),
                      (dict(n_seqs=-1), B.EINVAL), (dict(n_tokens=1 << 31), B.EUNSUPPORTED)):
         with pytest.raises(B.SplitKVError) as e:
             B.splitkv_paged_append(desc(), **{**good, **kw}, stream=0)
