@@ -27,8 +27,12 @@ using sm100::ex2_approx;
 constexpr int kTile = 16;          // keys of a unit
 constexpr int kMaxParts = 192;     // most blocks that share the work: counters and partial slots of the workspace
 constexpr size_t kCounterBytes = 1024;
-constexpr int kSegmentCost = 4;    // units that the beginning of a segment counts
-constexpr int kAlone = 6;          // tiles a warp may have for a block to take a whole segment, without a join of blocks
+// Units that the beginning of a segment counts. 64 sequences of 1 .. 16384 keys, 8 kv heads: 0 units 168 us, 2: 98, 4: 84,
+// 8: 85, 16: 86 (with 0 the short ones pile up on a few warps).
+constexpr int kSegmentCost = 4;
+// Units a warp may have for a block to take a whole segment, without a join of blocks. One sequence, 4 kv heads, 12
+// warps: 200 keys 9.6 us so and 13.5 us split, 600 keys 13.0 both, 1000 keys 16.0 and 13.1.
+constexpr int kAlone = 3;
 constexpr float kLazy = 8.f;       // log2 units a score may exceed the reference before the reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kNone = ~0u;
@@ -826,45 +830,56 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
     }
 }
 
-template <typename T, int DP, int NT, int W>
-cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
-                   const int32_t* table, const int32_t* seq_len, const int32_t* pages, int32_t n_select, void* o,
-                   float* lse, int32_t* status, void* ws, cudaStream_t st) {
+// One compiled kernel: type, channels (rounded up), tiles of 8 query rows and warps of a block.
+template <typename T_, int DP_, int NT_, int W_>
+struct Variant {
+    using T = T_;
+    static constexpr int DP = DP_, NT = NT_, W = W_;
     using P = Partial<DP, 8 * NT>;
-    int sms = 0;
-    cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return e;
-    constexpr size_t kFixed = sizeof(P) * W * 2 + Frag<T, DP, NT>::kShared * 512 * W;
-    const size_t smem = kFixed + sizeof(int32_t) * std::max(m.n_seqs + 1, W * 36);
-    auto kern = decode_kernel<T, DP, NT, W>;
-    static SmemGrants granted;
-    e = allow_smem((const void*)kern, kFixed + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), granted);
-    if (e != cudaSuccess) return e;
-    const int grid = std::min(sms, kMaxParts);
-    return note_error(launch_overlapped(kern, grid, W * 32, smem, st, m, (const T*)q, q_stride, (const T*)k_cache,
-                                        (const T*)v_cache, table, seq_len, pages, n_select, (T*)o, lse, status,
-                                        (uint32_t*)ws, (char*)ws + kCounterBytes),
-                      "paged decode");
+    static constexpr size_t kWorkspace = kCounterBytes + sizeof(P) * kMaxParts * 2;
+    static constexpr size_t kShared = sizeof(P) * W * 2 + Frag<T, DP, NT>::kShared * 512 * W;
+};
+
+// fn(variant) with the variant for a cache: the scratch's size and the launch come from the same choice.
+//   More than 8 query heads a kv head: 16 rows a warp read K and V once (4 x 60000 keys, 32/2 heads, d 128: 58 us; 8 rows
+//   a warp, the second half from L2: 66 us). float32 has no registers for 16 rows.
+//   Warps: as many as leave the registers for a tile of K and of V in flight (d 64, 8 rows: 12 warps 51 us, 16 warps
+//   of fewer registers 57 us; 16 rows: 12 warps 36 us, 8 warps 40 us. d 128, 16 rows: 8 warps 58 us, 10 spill, 96 us).
+template <typename F>
+auto with_variant(const PagedMeta& m, F&& fn) {
+    if (m.dtype == SPLITKV_F32) return m.d <= 64 ? fn(Variant<float, 64, 1, 12>{}) : fn(Variant<float, 128, 1, 8>{});
+    if (m.group > 8)
+        return m.d <= 64 ? fn(Variant<__nv_bfloat16, 64, 2, 12>{}) : fn(Variant<__nv_bfloat16, 128, 2, 8>{});
+    return m.d <= 64 ? fn(Variant<__nv_bfloat16, 64, 1, 12>{}) : fn(Variant<__nv_bfloat16, 128, 1, 12>{});
 }
 
 }  // namespace
 
 size_t paged_decode_workspace(const PagedMeta& m) {
-    const size_t rows = m.group > 8 && m.dtype == SPLITKV_BF16 ? 16 : 8, channels = m.d <= 64 ? 64 : 128;
-    return kCounterBytes + rows * (channels + 2) * sizeof(float) * kMaxParts * 2;
+    return with_variant(m, [](auto v) { return decltype(v)::kWorkspace; });
 }
 
 cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,
                                 const void* v_cache, const int32_t* table, const int32_t* seq_len,
                                 const int32_t* pages, int32_t n_select, void* o, float* lse, int32_t* status, void* ws,
                                 cudaStream_t st) {
-#define SPLITKV_DECODE(T, DP, NT, W) \
-    launch<T, DP, NT, W>(m, q, q_stride, k_cache, v_cache, table, seq_len, pages, n_select, o, lse, status, ws, st)
-    if (m.dtype == SPLITKV_F32) return m.d <= 64 ? SPLITKV_DECODE(float, 64, 1, 12) : SPLITKV_DECODE(float, 128, 1, 8);
-    if (m.group > 8)
-        return m.d <= 64 ? SPLITKV_DECODE(__nv_bfloat16, 64, 2, 12) : SPLITKV_DECODE(__nv_bfloat16, 128, 2, 8);
-    return m.d <= 64 ? SPLITKV_DECODE(__nv_bfloat16, 64, 1, 16) : SPLITKV_DECODE(__nv_bfloat16, 128, 1, 12);
-#undef SPLITKV_DECODE
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    return with_variant(m, [&](auto v) {
+        using V = decltype(v);
+        using T = typename V::T;
+        auto kern = decode_kernel<T, V::DP, V::NT, V::W>;
+        static SmemGrants granted;
+        const cudaError_t e =
+            allow_smem((const void*)kern, V::kShared + sizeof(int32_t) * (SPLITKV_PAGED_MAX_SEQS + 1), granted);
+        if (e != cudaSuccess) return e;
+        const size_t smem = V::kShared + sizeof(int32_t) * std::max(m.n_seqs + 1, V::W * 36);
+        return note_error(launch_overlapped(kern, std::min(sms, kMaxParts), V::W * 32, smem, st, m, (const T*)q, q_stride,
+                                            (const T*)k_cache, (const T*)v_cache, table, seq_len, pages, n_select, (T*)o,
+                                            lse, status, (uint32_t*)ws, (char*)ws + kCounterBytes),
+                          "paged decode");
+    });
 }
 
 }  // namespace splitkv
