@@ -15,6 +15,8 @@ namespace splitkv {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Blocks of the streaming kernels: 128 threads 140 us, 256 143, 512 149 (35k tokens, 32/4 heads).
+constexpr int kStreamThreads = 128, kStreamWarps = kStreamThreads / 32;
 constexpr int kMaxPage = 1024;
 
 // Where token i goes. Padding and tokens out of range have page -1; the order is checked against the token
@@ -288,13 +290,13 @@ struct Units {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     after_previous();
     if (status_bad(status)) return;
     const int lane = threadIdx.x & 31;
     const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
     const Units Q(m.hq, 4 * L.rows), KV(m.hkv, 2 * L.rows);
-    int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5);
     const int64_t q_units = a.q ? Q.of(a.n_tokens) : 0;
     const bool queries = unit < q_units;
     const Units U = queries ? Q : KV;
@@ -398,9 +400,9 @@ __device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const Append
 
 // Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's 32, at one kv head.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__global__ void __launch_bounds__(kStreamThreads, 8) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * 32;
+    const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * 32;
     const int32_t g = (int32_t)(unit % m.hkv);
     const Lanes L = lanes_of<T>(m.d, 0, 0, lane);
     uint32_t firsts = page_firsts(m, a, i0, 32, lane, false, status);
@@ -657,14 +659,17 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     const int64_t kv_blocks = (a.n_tokens + slice - 1) / slice;
     const int turned = a.rope_dim / 2 / Vec<T>::kN, rows = 32 / (turned + ((m.d - a.rope_dim) / Vec<T>::kN + 1) / 2);
     const int64_t all = a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv);
-    if (all / rows >= kSms * 32) {  // several times what the SMs hold at once
+    // From about what the SMs hold at once the rows stream. 32/4 heads, d 128, 500 tokens (5000 warps' rows): pages of 64
+    // 8.9 us so and 13.5 page by page, pages of 16 11.4 and 9.6; 2000 tokens 14.0 and 19.1, 16.4 and 20.3; 8000 tokens 37
+    // and 66, 37 and 71.
+    if (all / rows >= kSms * 32) {
         const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
         const int64_t slices = (a.n_tokens + 31) / 32 * m.hkv;
-        cudaError_t e = launch_overlapped(append_stream_kernel<T>, (units + kWarps - 1) / kWarps, kThreads, 0, st, m, a,
-                                          status);
+        cudaError_t e = launch_overlapped(append_stream_kernel<T>, (units + kStreamWarps - 1) / kStreamWarps,
+                                          kStreamThreads, 0, st, m, a, status);
         if (e == cudaSuccess && a.k_bounds)
-            e = launch_overlapped(append_bounds_stream_kernel<T>, (slices + kWarps - 1) / kWarps, kThreads, 0, st, m, a,
-                                  status);
+            e = launch_overlapped(append_bounds_stream_kernel<T>, (slices + kStreamWarps - 1) / kStreamWarps,
+                                  kStreamThreads, 0, st, m, a, status);
         return note_error(e, "paged append");
     }
     const int32_t heads = std::min(m.hq, rows);
