@@ -246,8 +246,10 @@ struct Frag<float, DP, NT> {
             }
         }
     }
-    // acc += a b over 8 channels, a [16 x 8] as four values a lane. kCut: a may be as large as the type goes. kInf: a or b
-    // may be infinite and have no halves then; only the product of the high ones sees it.
+    // acc += a b over 8 channels, a [16 x 8] as four values a lane. Formed apart and added in float32: the tensor core cuts
+    // what its sums do not hold, always toward zero, and over a long row that would add up (1.3e-6 of o over 10^4 keys;
+    // 3e-7 so). kCut: a may be as large as the type goes. kInf: a or b may be infinite and have no halves then; only the
+    // product of the high ones sees it.
     template <bool kCut, bool kInf>
     static __device__ __forceinline__ void product(float (&acc)[NT][4], const float (&a)[4], const float (&b0)[NT],
                                                    const float (&b1)[NT]) {
@@ -266,9 +268,12 @@ struct Frag<float, DP, NT> {
             uint32_t f0 = h0, f1 = h1;
             if (kInf && !isfinite(b0[n])) l0 = f0 = 0;
             if (kInf && !isfinite(b1[n])) l1 = f1 = 0;
-            mma_tf32(acc[n], lo, f0, f1);
-            mma_tf32(acc[n], fin, l0, l1);
-            mma_tf32(acc[n], hi, h0, h1);
+            float d[4] = {};
+            mma_tf32(d, lo, f0, f1);
+            mma_tf32(d, fin, l0, l1);
+            mma_tf32(d, hi, h0, h1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] += d[i];
         }
     }
     __device__ __forceinline__ void scores(float (&s)[NT][4]) const {
@@ -282,7 +287,10 @@ struct Frag<float, DP, NT> {
     }
     template <bool kInf>
     __device__ __forceinline__ void sums(float (&s)[NT][4]) const {
-        float a[2][NT][4] = {};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j) {
             float b[4][NT];
@@ -291,13 +299,9 @@ struct Frag<float, DP, NT> {
                 const float4 y = q[(n * DP / 16 + j) * 32 + (threadIdx.x & 31)];
                 b[0][n] = y.x, b[1][n] = y.y, b[2][n] = y.z, b[3][n] = y.w;
             }
-            product<kInf, kInf>(a[0], {k[j][0].x, k[j][1].x, k[j][0].y, k[j][1].y}, b[0], b[1]);
-            product<kInf, kInf>(a[1], {k[j][0].z, k[j][1].z, k[j][0].w, k[j][1].w}, b[2], b[3]);
+            product<kInf, kInf>(s, {k[j][0].x, k[j][1].x, k[j][0].y, k[j][1].y}, b[0], b[1]);
+            product<kInf, kInf>(s, {k[j][0].z, k[j][1].z, k[j][0].w, k[j][1].w}, b[2], b[3]);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] = a[0][n][i] + a[1][n][i];
     }
     __device__ __forceinline__ void values(const float (&p)[NT][4], int lane) {
         const int g = lane >> 2, t = lane & 3;
@@ -316,22 +320,17 @@ struct Frag<float, DP, NT> {
 #pragma unroll
             for (int c0 = 0; c0 < DP / 32; ++c0) {
                 const float4 &y = v[c0][2 * x], &z = v[c0][2 * x + 1];
-                float acc[NT][4];
+                float acc[2][NT][4];
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < 4; ++i) acc[0][n][i] = o[n][2 * c0][i], acc[1][n][i] = o[n][2 * c0 + 1][i];
+                product<true, false>(acc[0], {y.x, y.y, z.x, z.y}, b0, b1);
+                product<true, false>(acc[1], {y.z, y.w, z.z, z.w}, b0, b1);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[n][i] = o[n][2 * c0 + w][i];
-                    if (w == 0)
-                        product<true, false>(acc, {y.x, y.y, z.x, z.y}, b0, b1);
-                    else
-                        product<true, false>(acc, {y.z, y.w, z.z, z.w}, b0, b1);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[n][2 * c0 + w][i] = acc[n][i];
-                }
+                    for (int i = 0; i < 4; ++i) o[n][2 * c0][i] = acc[0][n][i], o[n][2 * c0 + 1][i] = acc[1][n][i];
             }
         }
     }
