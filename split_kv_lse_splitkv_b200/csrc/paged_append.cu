@@ -33,6 +33,28 @@ __device__ TokenPlace token_place(const PagedMeta& m, const AppendArgs& a, int64
     return t;
 }
 
+// The nearest token before i (kAfter: after i) that is not padding, or -1, on a whole warp with the same i in each lane: 256
+// tokens a step, because a padded batch has long runs of padding (one thread, token by token: 8 rows padded to 4096, a third
+// of them tokens, 32/4 heads, d 128: 400 us; so: 108). Not inlined: it is rarely called, and the callers need the registers.
+template <bool kAfter>
+__device__ __noinline__ int64_t token_beside(const AppendArgs& a, int64_t i, int lane) {
+    constexpr int kLook = 8;
+    for (int64_t base = 1; kAfter ? i + base < a.n_tokens : i - base >= 0; base += kLook * 32) {
+        uint32_t real[kLook];
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+            const int64_t p = kAfter ? i + base + u * 32 + lane : i - base - u * 32 - lane;
+            real[u] = p >= 0 && p < a.n_tokens && __ldg(a.token_seq + p) >= 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+            const uint32_t found = __ballot_sync(0xffffffffu, real[u]);
+            if (found) return kAfter ? i + base + u * 32 + __ffs(found) - 1 : i - base - u * 32 - __ffs(found) + 1;
+        }
+    }
+    return -1;
+}
+
 // Channel i of a row, rotated at the row of cosines and sines `cs` (null: as it is).
 template <typename T>
 __device__ T rotated(const AppendArgs& a, const T* x, int32_t i, const float* cs) {
@@ -52,9 +74,8 @@ __global__ void __launch_bounds__(128) append_rows_kernel(PagedMeta m, AppendArg
     if (status_bad(status)) return;
     const int64_t i = blockIdx.x;
     const TokenPlace t = token_place(m, a, i, status);
-    if (t.seq >= 0 && threadIdx.x == 0) {
-        int64_t p = i - 1;
-        while (p >= 0 && a.token_seq[p] < 0) --p;
+    if (t.seq >= 0 && threadIdx.x < 32) {
+        const int64_t p = token_beside<false>(a, i, threadIdx.x);
         if (p >= 0 && (a.token_seq[p] > t.seq || (a.token_seq[p] == t.seq && a.token_pos[p] >= t.pos)))
             raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
     }
@@ -80,9 +101,8 @@ __global__ void __launch_bounds__(128) append_bounds_kernel(PagedMeta m, AppendA
     const int64_t i = blockIdx.x;
     const TokenPlace t = token_place(m, a, i, status);
     if (t.page < 0) return;
-    int64_t n = i + 1;
-    while (n < a.n_tokens && a.token_seq[n] < 0) ++n;
-    if (n < a.n_tokens && a.token_seq[n] == t.seq && a.token_pos[n] >> m.page_shift == t.pos >> m.page_shift) return;
+    const int64_t n = token_beside<true>(a, i, threadIdx.x & 31);
+    if (n >= 0 && a.token_seq[n] == t.seq && a.token_pos[n] >> m.page_shift == t.pos >> m.page_shift) return;
     const int32_t last = t.pos & (m.page - 1);
     for (int32_t e = threadIdx.x; e < m.hkv * m.d; e += 128) {
         const int32_t g = e / m.d, c = e % m.d;
@@ -265,21 +285,41 @@ __device__ __forceinline__ void append_queries(const PagedMeta& m, const AppendA
     }
 }
 
-// Whether token i, of sequence seq >= 0, comes after the token before it that is not padding (else the status bit).
-__device__ __forceinline__ void check_order(const AppendArgs& a, int64_t i, int32_t seq, int32_t pos, int32_t* status,
-                                            int32_t& before, int32_t& before_pos) {
-    before = before_pos = -1;
-    for (int64_t p = i - 1; p >= 0; --p)
-        if ((before = __ldg(a.token_seq + p)) >= 0) {
-            before_pos = __ldg(a.token_pos + p);
-            break;
+// Which of the `slice` <= 32 tokens from i0 on (a lane each) are the first of the call in their page. `report`: say what is
+// wrong with them, their order included, in the status word.
+__device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const AppendArgs& a, int64_t i0, int32_t slice,
+                                                int lane, bool report, int32_t* status) {
+    if (i0 >= a.n_tokens) return 0;
+    const int64_t i = i0 + lane;
+    const bool mine = lane < slice && i < a.n_tokens;
+    const int32_t seq = mine ? __ldg(a.token_seq + i) : -1, pos = mine ? __ldg(a.token_pos + i) : 0;
+    int32_t before = i0 > 0 ? __ldg(a.token_seq + i0 - 1) : -1, before_pos = i0 > 0 ? __ldg(a.token_pos + i0 - 1) : -1;
+    const uint32_t real = __ballot_sync(0xffffffffu, seq >= 0), below = real & ((1u << lane) - 1);
+    if (!real) return 0;
+    if (i0 > 0 && before < 0) {  // padding before the slice
+        const int64_t p = token_beside<false>(a, i0 - 1, lane);
+        if (p >= 0) before = __ldg(a.token_seq + p), before_pos = __ldg(a.token_pos + p);
+    }
+    const int from = below ? 31 - __clz(below) : 0;
+    const int32_t s = __shfl_sync(0xffffffffu, seq, from), p = __shfl_sync(0xffffffffu, pos, from);
+    if (below) before = s, before_pos = p;
+    bool first = seq >= 0;
+    if (first) {
+        if (report && (before > seq || (before == seq && before_pos >= pos))) raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
+        if (seq >= m.n_seqs || pos < 0 || pos >= (int64_t)m.max_pages * m.page || (a.rope && pos >= a.rope_len)) {
+            if (report) raise_status(status, SPLITKV_DEV_BAD_TOKEN);
+            first = false;
+        } else if (before == seq && before_pos >= 0 && before_pos >> m.page_shift == pos >> m.page_shift) {
+            first = false;
         }
-    if (before > seq || (before == seq && before_pos >= pos)) raise_status(status, SPLITKV_DEV_TOKEN_ORDER);
+    }
+    return __ballot_sync(0xffffffffu, first);
 }
 
 // Many tokens: rows by themselves. A unit is `most` rows: that many heads of one token, or all heads of several tokens
-// where they are few. A warp has a unit of queries, or one of keys and the same one of values. The bounds of the keys
-// follow in a launch of their own, from L2. (A page's rows and bounds in one block, as below, keep too few loads in
+// where they are few. A warp has a unit of queries, or one of keys and the same one of values. What is wrong with
+// the tokens' order is found, and the bounds of the keys are taken, in a launch of its own, from L2 (looking at the order
+// beside the rows costs 4 us of 140). (A page's rows and bounds in one block, as below, keep too few loads in
 // flight to fill the GPU: 35k tokens took 52 us for keys and values alone, against 23 us for their bytes.)
 struct Units {
     int32_t heads, tokens;  // of a unit
@@ -358,10 +398,6 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
     for (int k = 0; k < 2; ++k) {
         if (!in[k]) continue;
         const TokenPlace t = token_place(m, a, i[k], status);
-        if (h[k] == 0 && L.a == 0 && t.seq >= 0) {
-            int32_t before, before_pos;
-            check_order(a, i[k], t.seq, t.pos, status, before, before_pos);
-        }
         if (t.page < 0) continue;
         if (L.pair >= 0) {
             ang.load(a.rope + (int64_t)t.pos * a.rope_dim, a.rope_dim / 2, L.pair);
@@ -377,35 +413,21 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
     }
 }
 
-// Which of the 32 tokens from i0 on (a lane each) are the first of the call in their page. `report`: say what is wrong
-// with them, in the status word.
-__device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const AppendArgs& a, int64_t i0, int32_t slice,
-                                                int lane, bool report, int32_t* status) {
-    const int64_t i = i0 + lane;
-    const bool mine = lane < slice && i < a.n_tokens;
-    const int32_t seq = mine ? __ldg(a.token_seq + i) : -1, pos = seq >= 0 ? __ldg(a.token_pos + i) : 0;
-    bool first = seq >= 0;
-    if (first) {
-        int32_t before, before_pos;
-        check_order(a, i, seq, pos, report ? status : nullptr, before, before_pos);
-        if (seq >= m.n_seqs || pos < 0 || pos >= (int64_t)m.max_pages * m.page || (a.rope && pos >= a.rope_len)) {
-            if (report) raise_status(status, SPLITKV_DEV_BAD_TOKEN);
-            first = false;
-        } else if (before == seq && before_pos >= 0 && before_pos >> m.page_shift == pos >> m.page_shift) {
-            first = false;
-        }
-    }
-    return __ballot_sync(0xffffffffu, first);
+// Many tokens without bounds, second launch: what is wrong with the tokens, 32 a warp.
+__global__ void __launch_bounds__(kStreamThreads) append_order_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+    after_previous();
+    const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5);
+    page_firsts(m, a, unit * 32, 32, threadIdx.x & 31, true, status);
 }
 
 // Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's 32, at one kv head.
 template <typename T>
-__global__ void __launch_bounds__(kStreamThreads, 8) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * 32;
     const int32_t g = (int32_t)(unit % m.hkv);
     const Lanes L = lanes_of<T>(m.d, 0, 0, lane);
-    uint32_t firsts = page_firsts(m, a, i0, 32, lane, false, status);
+    uint32_t firsts = page_firsts(m, a, i0, 32, lane, g == 0, status);
     bool waited = false;
     if (!firsts) after_previous();
     for (; firsts; firsts &= firsts - 1) {
@@ -422,6 +444,11 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_bounds_stream_kernel
             const int end = stops ? __ffs(stops) - 1 : 32;
             last = max(last, __reduce_max_sync(0xffffffffu, in && lane < end ? q & (m.page - 1) : 0));
             if (stops) break;
+            if (!__any_sync(0xffffffffu, s >= 0)) {  // padding: on to what comes after it
+                const int64_t n = token_beside<true>(a, base + 31, lane);
+                if (n < 0) break;
+                base = n - 32;
+            }
         }
         if (!waited) after_previous();  // the keys
         waited = true;
@@ -664,11 +691,11 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     // and 66, 37 and 71.
     if (all / rows >= kSms * 32) {
         const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
-        const int64_t slices = (a.n_tokens + 31) / 32 * m.hkv;
+        const int64_t slices = (a.n_tokens + 31) / 32 * (a.k_bounds ? m.hkv : 1);
         cudaError_t e = launch_overlapped(append_stream_kernel<T>, (units + kStreamWarps - 1) / kStreamWarps,
                                           kStreamThreads, 0, st, m, a, status);
-        if (e == cudaSuccess && a.k_bounds)
-            e = launch_overlapped(append_bounds_stream_kernel<T>, (slices + kStreamWarps - 1) / kStreamWarps,
+        if (e == cudaSuccess)
+            e = launch_overlapped(a.k_bounds ? append_bounds_stream_kernel<T> : append_order_kernel, (slices + kStreamWarps - 1) / kStreamWarps,
                                   kStreamThreads, 0, st, m, a, status);
         return note_error(e, "paged append");
     }

@@ -365,6 +365,39 @@ def test_append_many_tokens(dtype, hq, hkv, d, rot, interleaved, page):
     run_append(lens, new, hq, hkv, d, page, dtype, rot, interleaved, padding=(0, 7, 40, 41, 300), seed=d)
 
 
+@pytest.mark.parametrize("rot", [64, 10])
+@pytest.mark.parametrize("width", [600, 3000])
+def test_append_padded_batch(width, rot):
+    # Rows of `width` tokens, the shorter ones filled up: the token before a run of padding is looked for behind it.
+    new = [width, 1, 255, 256, 257, width - 1]
+    padding, at = [], 0
+    for n in new:
+        padding += range(at + n, at + width)
+        at += width
+    run_append([n + 5 for n in new], new, 8, 2, 64, 16, BF, rot, False, padding=padding)
+    # A page's tokens on both sides of a run.
+    run_append([width + 20], [width + 20], 8, 2, 64, 16, BF, rot, False, padding=range(5, 5 + 2 * width))
+
+
+@pytest.mark.parametrize("rot", [64, 10])
+@pytest.mark.parametrize("tokens", [2, 9000])
+@pytest.mark.parametrize("run", [31, 256, 5000])
+def test_append_order_is_checked_across_padding(run, tokens, rot):
+    c = Case([tokens], 8, 2, 64, 16)
+    kv = PagedKV(8, 2, 64, 16, max_seqs=1, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v)
+    pos = torch.arange(tokens, dtype=torch.int32)
+    pos = torch.cat((pos[:tokens // 2], torch.zeros(run, dtype=torch.int32), pos[tokens // 2 :]))
+    seq = torch.zeros(tokens + run, dtype=torch.int32)
+    seq[tokens // 2 : tokens // 2 + run] = -1
+    x = torch.zeros(tokens + run, 2, 64, dtype=BF, device="cuda")
+    rope = rope_table(tokens, rot)
+    kv.append(x, x, c.table, seq.cuda(), pos.cuda(), rope=rope)
+    assert kv.status_value() == 0
+    pos[tokens // 2 + run] = tokens // 2 - 1
+    kv.append(x, x, c.table, seq.cuda(), pos.cuda(), rope=rope)
+    assert kv.status_value() == B.DEV_TOKEN_ORDER
+
+
 def test_append_many_tokens_orders_and_options():
     run_append([3000, 2000], [2500, 2000], 8, 2, 128, 32, BF, 128, False, order="positions")
     run_append([3000, 2000], [2500, 2000], 8, 2, 128, 32, F32, 128, True, order="gaps")
