@@ -343,7 +343,7 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
  * log-sum-exp merge), and splitkv_paged_select picks, for each token and kv head, the pages that a
  * cheap score ranks highest, so that splitkv_paged_decode reads those pages only.
  *
- *   k_cache, v_cache  element (page, g, t, i) of page `page`, kv head g, position t within the page and
+ *   k_cache, v_cache  (two tensors) element (page, g, t, i) of page `page`, kv head g, position t within the page and
  *                     channel i at page*page_stride + g*head_stride + t*token_stride + i (elements):
  *                     any order of the three outer dimensions, no two of them overlapping.
  *   k_bounds          [n_pages, Hkv, 2, d], dense, the problem's dtype: the smallest and the largest
@@ -355,6 +355,7 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
  *                     times with the lengths that each of them sees.
  *   q, o              [n_seqs, Hq, d]; q's tokens are q_stride elements apart (a slice of a fused
  *                     projection), each token's heads dense; o and lse [n_seqs, Hq] are dense.
+ * What a call writes lies apart from what it reads, and its outputs from each other (EINVAL where the call can tell).
  * Pointers are 16-byte aligned and every stride a multiple of 16 bytes (k_cache, v_cache, k_bounds, q, k,
  * v, o, rope and workspaces; lists and tables of int32 need their own alignment only). Sums, maxima and
  * partial results are float32; the choice of pages is that of float64 scores, so that no rounding decides it.
@@ -376,7 +377,7 @@ typedef struct {
     int32_t head_dim;     /* d: bf16 a multiple of 8, f32 a multiple of 4; 8..128                 */
     int32_t page_size;    /* positions per page: a power of two, 1..1024                          */
     int64_t n_pages;      /* pages of the cache                                                   */
-    int32_t max_pages;    /* entries of a page-table row: the longest sequence is max_pages pages */
+    int32_t max_pages;    /* entries of a page-table row: max_pages * page_size < 2^31 - 2048   */
     int64_t table_stride; /* entries from one row of the page table to the next, >= max_pages     */
     int64_t page_stride;  /* strides of k_cache and v_cache, in elements                          */
     int64_t head_stride;
@@ -395,7 +396,8 @@ size_t splitkv_paged_workspace_size(const splitkv_paged *paged, int32_t n_seqs);
  * Append: for each token i < n_tokens with token_seq_d[i] = b >= 0 and token_pos_d[i] = p, rotates its keys
  * and writes them and its values to position p of sequence b. token_seq_d[i] < 0 marks padding: nothing is
  * written to the cache. The other tokens must be strictly ascending by (b, p) (SPLITKV_DEV_TOKEN_ORDER):
- * no position is given twice.
+ * no position is given twice. The pages written belong to one sequence each, once in its row (shared pages are
+ * for reading).
  *   k, v   [n_tokens, Hkv, d], tokens k_stride and v_stride elements apart, each token's heads dense.
  *   q      [n_tokens, Hq, d] (q_stride) or NULL: rotated into q_out [n_tokens, Hq, d] (dense, apart from
  *          q, k and v). A padding token's queries are copied as they are.

@@ -445,7 +445,8 @@ int build_paged(const splitkv_paged* p, int64_t n_seqs, PagedMeta* m) {
     const int32_t vec = p->dtype == SPLITKV_BF16 ? 8 : 4;  // elements of 16 bytes
     if (p->head_dim % vec || p->head_dim > 128 || p->head_dim < 8) return SPLITKV_EUNSUPPORTED;
     if (p->page_size > 1024 || (p->page_size & (p->page_size - 1))) return SPLITKV_EUNSUPPORTED;
-    if (p->n_pages > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX) return SPLITKV_EUNSUPPORTED;
+    // Positions, rounded up to a page and a tile, in 31 bits.
+    if (p->n_pages > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX - 2048) return SPLITKV_EUNSUPPORTED;
     if (n_seqs > SPLITKV_PAGED_MAX_SEQS || p->n_q_heads > 32768) return SPLITKV_EUNSUPPORTED;
     // The units of work (16 positions of a sequence, kv head and 8 query rows) are counted in 31 bits.
     if (n_seqs * (((int64_t)p->max_pages * p->page_size + 15) / 16 + 4) >
@@ -487,6 +488,14 @@ bool rows_ok(const PagedMeta& m, const void* x, int64_t n, int64_t stride, int32
     return x && aligned16(x) && (n <= 1 || (stride >= (int64_t)heads * m.d && stride % vec == 0 && stride <= (int64_t)1 << 32));
 }
 
+// Bytes from the first to the last element of such a tensor; whether two ranges of bytes meet.
+int64_t rows_bytes(const PagedMeta& m, int64_t n, int64_t stride, int32_t heads) {
+    return ((n > 1 ? (n - 1) * stride : 0) + (int64_t)heads * m.d) * (m.dtype == SPLITKV_BF16 ? 2 : 4);
+}
+bool overlap(const void* x, int64_t x_bytes, const void* y, int64_t y_bytes) {
+    return (const char*)x < (const char*)y + y_bytes && (const char*)y < (const char*)x + x_bytes;
+}
+
 }  // namespace
 
 SPLITKV_API size_t splitkv_paged_workspace_size(const splitkv_paged* paged, int32_t n_seqs) {
@@ -517,16 +526,14 @@ SPLITKV_API int splitkv_paged_append(const splitkv_paged* paged, int32_t n_seqs,
     if (n_tokens == 0) return SPLITKV_OK;
     if (!rows_ok(m, k, n_tokens, k_stride, m.hkv) || !rows_ok(m, v, n_tokens, v_stride, m.hkv)) return SPLITKV_EINVAL;
     if (q && (!rows_ok(m, q, n_tokens, q_stride, m.hq) || !q_out || !aligned16(q_out))) return SPLITKV_EINVAL;
-    if (!page_table_d || !token_seq_d || !token_pos_d || !k_cache || !v_cache) return SPLITKV_EINVAL;
+    if (!page_table_d || !token_seq_d || !token_pos_d || !k_cache || !v_cache || k_cache == v_cache) return SPLITKV_EINVAL;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_bounds) || !aligned16(rope)) return SPLITKV_EINVAL;
-    if (q) {  // q_out is written while other blocks still read q, k and v: refuse any overlap of their ranges
-        const int64_t e = m.dtype == SPLITKV_BF16 ? 2 : 4;
-        const char* y = (const char*)q_out;
-        auto over = [&](const void* x, int64_t stride, int32_t heads) {
-            const int64_t bytes = ((n_tokens - 1) * (n_tokens > 1 ? stride : 0) + (int64_t)heads * m.d) * e;
-            return (const char*)x < y + n_tokens * m.hq * m.d * e && y < (const char*)x + bytes;
-        };
-        if (over(q, q_stride, m.hq) || over(k, k_stride, m.hkv) || over(v, v_stride, m.hkv)) return SPLITKV_EINVAL;
+    if (q) {  // q_out is written while other blocks still read q, k and v
+        const int64_t out = rows_bytes(m, n_tokens, (int64_t)m.hq * m.d, m.hq);
+        if (overlap(q_out, out, q, rows_bytes(m, n_tokens, q_stride, m.hq)) ||
+            overlap(q_out, out, k, rows_bytes(m, n_tokens, k_stride, m.hkv)) ||
+            overlap(q_out, out, v, rows_bytes(m, n_tokens, v_stride, m.hkv)))
+            return SPLITKV_EINVAL;
     }
     const AppendArgs a{n_tokens, q,           k,          v,           q_stride,    k_stride, v_stride,
                        rope,     rope_dim,    interleaved, rope_len,   page_table_d, token_seq_d, token_pos_d,
@@ -544,12 +551,17 @@ SPLITKV_API int splitkv_paged_decode(const splitkv_paged* paged, int32_t n_seqs,
     int rc = build_paged(paged, n_seqs, &m);
     if (rc) return rc;
     if (!status_d || (pages_d && n_select < 1)) return SPLITKV_EINVAL;
+    if (pages_d && n_select > (1 << 30) / m.hkv) return SPLITKV_EUNSUPPORTED;
     if (n_seqs == 0) return SPLITKV_OK;
     if (!rows_ok(m, q, n_seqs, q_stride, m.hq) || !k_cache || !v_cache || !page_table_d || !seq_len_d || !o || !lse)
         return SPLITKV_EINVAL;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return SPLITKV_EINVAL;
     if (!workspace_d || workspace_bytes < paged_decode_workspace(m)) return SPLITKV_ENOSPACE;
     if (!aligned16(workspace_d)) return SPLITKV_EINVAL;
+    const int64_t q_bytes = rows_bytes(m, n_seqs, q_stride, m.hq), o_bytes = rows_bytes(m, n_seqs, (int64_t)m.hq * m.d, m.hq);
+    const int64_t lse_bytes = (int64_t)n_seqs * m.hq * 4;
+    if (overlap(o, o_bytes, q, q_bytes) || overlap(lse, lse_bytes, q, q_bytes) || overlap(o, o_bytes, lse, lse_bytes))
+        return SPLITKV_EINVAL;
     return cuda_status(launch_paged_decode(m, q, q_stride, k_cache, v_cache, page_table_d, seq_len_d, pages_d,
                                            pages_d ? n_select : 0, o, lse, status_d, workspace_d,
                                            (cudaStream_t)stream));

@@ -98,6 +98,7 @@ def desc(**kw):
     (dict(n_pages=0), B.EINVAL),
     (dict(max_pages=0), B.EINVAL),
     (dict(max_pages=1 << 28), B.EUNSUPPORTED),                             # a sequence of 2^32 positions
+    (dict(page_size=1, max_pages=(1 << 31) - 1, n_kv_heads=1), B.EUNSUPPORTED),  # rounded up to a tile: 2^31 positions
     (dict(table_stride=3), B.EINVAL),
     (dict(scale=0.0), B.EINVAL),
     (dict(scale=float("nan")), B.EINVAL),
@@ -150,6 +151,29 @@ def test_decode_refusals():
     assert e.value.code == B.EUNSUPPORTED
     # No sequence: nothing to do, no tensor is looked at.
     B.splitkv_paged_decode(desc(), 0, **{k: None for k in good} | dict(q_stride=0, n_select=0, status=f), stream=0)
+
+
+def test_decode_outputs_lie_apart():
+    f = [torch.empty(1 << 16, dtype=torch.int32) for _ in range(7)]
+    ws = torch.empty(B.splitkv_paged_workspace_size(desc(), 4), dtype=torch.uint8)
+    good = dict(q=f[0], q_stride=512, k_cache=f[1], v_cache=f[2], page_table=f[3], seq_len=f[3], pages=None, n_select=0,
+                o=f[4], lse=f[5], status=f[6], workspace=ws)
+    # q and o: 4 tokens of 1024 bytes; lse: 128 bytes.
+    for kw, code in ((dict(o=f[0]), B.EINVAL), (dict(o=f[0][1020:]), B.EINVAL), (dict(lse=f[0][4:]), B.EINVAL),
+                     (dict(lse=f[4][1023:]), B.EINVAL), (dict(q=f[4][512:], q_stride=1024), B.EINVAL),
+                     (dict(q=f[5][:16]), B.EINVAL), (dict(pages=f[3], n_select=(1 << 29) + 1), B.EUNSUPPORTED)):
+        with pytest.raises(B.SplitKVError) as e:
+            B.splitkv_paged_decode(desc(), 4, **{**good, **kw}, stream=0)
+        assert e.value.code == code, kw
+
+
+def test_append_caches_lie_apart():
+    f = [torch.empty(1 << 16, dtype=torch.int32) for _ in range(6)]
+    with pytest.raises(B.SplitKVError) as e:
+        B.splitkv_paged_append(desc(), n_seqs=4, n_tokens=5, q=None, q_stride=0, k=f[0], k_stride=128, v=f[1], v_stride=128,
+                               rope=None, rope_dim=0, rope_len=0, interleaved=0, page_table=f[2], token_seq=f[2],
+                               token_pos=f[2], q_out=None, k_cache=f[3], v_cache=f[3], k_bounds=None, status=f[4], stream=0)
+    assert e.value.code == B.EINVAL
 
 
 def test_append_refusals():
