@@ -50,10 +50,11 @@ class PagedKV:
     :meth:`select` only (``bounds=True`` allocates it).
 
     Every call takes a page table (int32 [n_seqs, up to max_pages]: row b lists the pages of sequence b) and is
-    enqueued on the current stream (``stream=``: on that one); none synchronizes (making the object does). Lengths, tables and token lists
-    are read on the device, so a call captured into a CUDA graph follows their values at each replay. The object's
-    scratch is shared by its decode calls: on a change of stream the new one waits for the old one, and a captured
-    call has scratch of its own. Errors that only the device sees collect in :attr:`status`.
+    enqueued on the current stream (``stream=``: on that one); none synchronizes (making the object does). Lengths,
+    tables and token lists are read on the device, so a call captured into a CUDA graph follows their values at each
+    replay. The object's scratch is shared by its decode calls: on a change of stream the new one waits for the old
+    one, and a captured call has scratch of its own. A stream given by its handle has to outlive the object. Results
+    carry no autograd history. Errors that only the device sees collect in :attr:`status`.
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, max_seqs, max_pages, n_pages=None, dtype=None,
@@ -266,21 +267,33 @@ class PagedKV:
         args = (layout, n, q.data_ptr(), qs, self._k_at, self._v_at, page_table.data_ptr(), seq_lens.data_ptr(), pages_at,
                 n_select, o.data_ptr(), lse.data_ptr(), self._status_at)
         if torch._C._cuda_isCurrentStreamCapturing():
-            # The graph may be replayed beside other work of this object: scratch of its own, its counters zeroed
-            # by the graph.
-            ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
-            ws[:_COUNTERS].zero_()
-            rc = _decode(*args, ws.data_ptr(), self._ws_bytes, raw)
+            # The graph may be replayed beside other work of this object.
+            rc = self._decode_apart(args, raw)
         else:
             with self._lock:
-                if raw != self._stream.cuda_stream:  # the scratch is used in turn
-                    now = torch.cuda.current_stream(self.device)
-                    now.wait_stream(self._stream)
-                    self._stream = now
-                rc = _decode(*args, self._ws_at, self._ws_bytes, raw)
+                other = raw != self._stream.cuda_stream  # the scratch is used in turn
+                if other and self._capturing(self._stream):
+                    rc = self._decode_apart(args, raw)  # to wait for that stream now would be to join its capture
+                else:
+                    if other:
+                        now = torch.cuda.current_stream(self.device)
+                        now.wait_stream(self._stream)
+                        self._stream = now
+                    rc = _decode(*args, self._ws_at, self._ws_bytes, raw)
         if rc:
             raise SplitKVError(rc, "splitkv_paged_decode")
         return o, lse
+
+    def _decode_apart(self, args, raw) -> int:
+        """With scratch of the call's own, its counters zeroed on the stream."""
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        ws[:_COUNTERS].zero_()
+        return _decode(*args, ws.data_ptr(), self._ws_bytes, raw)
+
+    @staticmethod
+    def _capturing(stream) -> bool:
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
 
     # -- host-side reads (synchronizing; for tests and reports)
     def status_value(self) -> int:

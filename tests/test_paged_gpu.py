@@ -591,6 +591,34 @@ def test_graphs_follow_their_inputs_and_share_nothing():
     c.kv.check_status()
 
 
+def test_an_eager_call_beside_a_capture_stays_out_of_it():
+    # The object's last eager call was on the stream that is being captured: an eager call on another stream runs at once.
+    c = Case([3000, 40], 8, 2, 64, 16)
+    want = [t.clone() for t in c.kv.decode(c.q, c.table, c.lens)]
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    t.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.kv.decode(c.q, c.table, c.lens)  # warm-up
+    o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s, capture_error_mode="relaxed"):
+        captured = c.kv.decode(c.q, c.table, c.lens)
+        c.kv.decode(c.q, c.table, c.lens, o=o, lse=lse, stream=t)
+        assert not c.kv._capturing(t)
+        t.synchronize()
+        with torch.cuda.stream(t):
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+            o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g.replay()
+        c.kv.decode(c.q, c.table, c.lens, stream=t)
+    torch.cuda.synchronize()
+    assert torch.equal(captured[0], want[0]) and torch.equal(captured[1], want[1]) and not o.any()
+    c.kv.check_status()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_a_serving_run(dtype):
     """Prompts appended (in two pieces), then tokens one by one as one captured step: append, select, sparse and full
