@@ -667,7 +667,7 @@ def test_a_serving_run(dtype):
     torch.cuda.current_stream().wait_stream(side)
     with torch.cuda.graph(graph):
         q, pages, sparse, full = step()
-    checker = type("C", (), dict(dtype=dtype, d=d, lens_l=[max(prompts) + steps]))
+    like_case = type("C", (), dict(dtype=dtype, d=d, lens_l=[max(prompts) + steps]))
     for t in range(steps):
         x.copy_(torch.stack([all_qkv[b][prompts[b] + t] for b in range(n)]).cuda())
         graph.replay()
@@ -683,8 +683,8 @@ def test_a_serving_run(dtype):
             assert np.abs(got - want).max() <= half_step(dtype) * np.abs(want).max() + 1e-5
         want = OP.select(f64(q), f64(kv.k_bounds), tn, now, page, n_select, 1, 1)
         assert np.array_equal(pages.cpu().numpy(), want)
-        Case.check(checker, *full, OP.decode(f64(q), kn, vn, tn, now, 1 / np.sqrt(d)))
-        Case.check(checker, *sparse, OP.decode(f64(q), kn, vn, tn, now, 1 / np.sqrt(d), want))
+        Case.check(like_case, *full, OP.decode(f64(q), kn, vn, tn, now, 1 / np.sqrt(d)))
+        Case.check(like_case, *sparse, OP.decode(f64(q), kn, vn, tn, now, 1 / np.sqrt(d), want))
 
 
 def test_no_sequences_and_no_tokens():
