@@ -30,9 +30,11 @@ constexpr size_t kCounterBytes = 1024;
 // Units that the beginning of a segment counts. 64 sequences of 1 .. 16384 keys, 8 kv heads: 0 units 168 us, 2: 98, 4: 84,
 // 8: 85, 16: 86 (with 0 the short ones pile up on a few warps).
 constexpr int kSegmentCost = 4;
-// Units a warp may have for a block to take a whole segment, without a join of blocks. One sequence, 4 kv heads, 12
-// warps: 200 keys 9.6 us so and 13.5 us split, 600 keys 13.0 both, 1000 keys 16.0 and 13.1.
-constexpr int kAlone = 3;
+// Most units of a segment that a block takes whole, without a join of blocks. One sequence, 4 kv heads, 8 warps: 333 keys
+// (25 units) 10.2 us so and 11.4 us split, 440 keys 11.1 and 11.4, 500 keys (36 units) 11.6 and 11.2; d 64, 12 warps: 440
+// keys 9.2 and 10.2, 500 keys 9.6 and 10.4. float32, d 64: 320 keys (24 units) 11.8 both, 380 keys 13.1 and 12.1.
+template <typename T, int W>
+constexpr int kAlone = sizeof(T) == 4 ? 24 : W > 10 ? 36 : 32;
 constexpr float kLazy = 8.f;       // log2 units a score may exceed the reference before the reference moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kNone = ~0u;
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
             most = max(most, x);
         }
         empties = __syncthreads_or(none);
-        widest = __syncthreads_or(most > kAlone * W) ? INT32_MAX : 0;
+        widest = __syncthreads_or(most > kAlone<T, W>) ? INT32_MAX : 0;
         if (warp == 0) {
             int32_t carry = 0;
             for (int b0 = 0; b0 < m.n_seqs; b0 += 32) {
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         }
     // This block's part [c_lo, c_hi) of the line, and each warp's part of it.
     uint32_t c_lo = min(blockIdx.x * L.per_part, L.total), c_hi = min(c_lo + L.per_part, L.total);
-    if (widest <= kAlone * W && L.n_seqs * L.per_seq <= gridDim.x) {  // a block per segment
+    if (widest <= kAlone<T, W> && L.n_seqs * L.per_seq <= gridDim.x) {  // a block per segment
         const uint32_t b = blockIdx.x / L.per_seq;
         if (b >= L.n_seqs) return;
         const uint32_t width = prefix[b + 1] - prefix[b];
@@ -839,23 +841,33 @@ struct Variant {
     static constexpr size_t kShared = sizeof(P) * W * 2 + Frag<T, DP, NT>::kShared * 512 * W;
 };
 
-// fn(variant) with the variant for a cache: the scratch's size and the launch come from the same choice.
+// fn(variant) with the variant for a cache: the scratch's size and the launch come from the same choice. `units`: the most
+// units an SM may get, by the shapes; variants that it chooses between differ in warps only, which the scratch does not see.
 //   More than 8 query heads a kv head: 16 rows a warp read K and V once (4 x 60000 keys, 32/2 heads, d 128: 58 us; 8 rows
 //   a warp, the second half from L2: 66 us). float32 has no registers for 16 rows.
 //   Warps: as many as leave the registers for a tile of K and of V in flight (d 64, 8 rows: 12 warps 51 us, 16 warps
 //   of fewer registers 57 us; 16 rows: 12 warps 36 us, 8 warps 40 us. d 128, 16 rows: 8 warps 58 us, 10 spill, 96 us).
+//   Where there is little to read, 8: fewer parts to join, no spills (d 128, 4 kv heads: 1000 keys 13.1 us with 12
+//   warps, 11.7 with 8; 32768 keys, 55 units an SM, 23.9 and 22.5; 2 x 60000 keys, 203, 50.0 and 49.8; 8 x 131071, 1771,
+//   322 and 330. float32, d 64, 4 kv heads: 27 units 17.6 and 16.7; 55, 27.4 and 27.9; 101, 38.5 and 41.6).
+constexpr int64_t kFewBf16 = 400, kFewF32 = 40;
+
 template <typename F>
-auto with_variant(const PagedMeta& m, F&& fn) {
-    if (m.dtype == SPLITKV_F32) return m.d <= 64 ? fn(Variant<float, 64, 1, 12>{}) : fn(Variant<float, 128, 1, 8>{});
-    if (m.group > 8)
-        return m.d <= 64 ? fn(Variant<__nv_bfloat16, 64, 2, 12>{}) : fn(Variant<__nv_bfloat16, 128, 2, 8>{});
-    return m.d <= 64 ? fn(Variant<__nv_bfloat16, 64, 1, 12>{}) : fn(Variant<__nv_bfloat16, 128, 1, 12>{});
+auto with_variant(const PagedMeta& m, int64_t units, F&& fn) {
+    using B = __nv_bfloat16;
+    if (m.dtype == SPLITKV_F32) {
+        if (m.d > 64) return fn(Variant<float, 128, 1, 8>{});
+        return units <= kFewF32 ? fn(Variant<float, 64, 1, 8>{}) : fn(Variant<float, 64, 1, 12>{});
+    }
+    if (m.group > 8) return m.d <= 64 ? fn(Variant<B, 64, 2, 12>{}) : fn(Variant<B, 128, 2, 8>{});
+    if (m.d <= 64) return fn(Variant<B, 64, 1, 12>{});
+    return units <= kFewBf16 ? fn(Variant<B, 128, 1, 8>{}) : fn(Variant<B, 128, 1, 12>{});
 }
 
 }  // namespace
 
 size_t paged_decode_workspace(const PagedMeta& m) {
-    return with_variant(m, [](auto v) { return decltype(v)::kWorkspace; });
+    return with_variant(m, 0, [](auto v) { return decltype(v)::kWorkspace; });
 }
 
 cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,
@@ -865,7 +877,9 @@ cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_str
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    return with_variant(m, [&](auto v) {
+    const int64_t positions = (int64_t)(pages ? std::min(n_select, m.max_pages) : m.max_pages) * m.page;
+    const int64_t rows = (int64_t)m.n_seqs * m.hkv * ((m.group + 7) / 8);
+    return with_variant(m, rows * ((positions + kTile - 1) / kTile) / sms, [&](auto v) {
         using V = decltype(v);
         using T = typename V::T;
         auto kern = decode_kernel<T, V::DP, V::NT, V::W>;
