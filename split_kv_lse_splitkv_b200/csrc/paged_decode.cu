@@ -842,18 +842,21 @@ struct Variant {
 };
 
 // fn(variant) with the variant for a cache: the scratch's size and the launch come from the same choice. `units`: the most
-// units an SM may get, by the shapes; variants that it chooses between differ in warps only, which the scratch does not see.
+// units an SM may get, by the shapes; `listed`: of pages in a list. Variants that these choose between differ in warps
+// only, which the scratch does not see.
 //   More than 8 query heads a kv head: 16 rows a warp read K and V once (4 x 60000 keys, 32/2 heads, d 128: 58 us; 8 rows
 //   a warp, the second half from L2: 66 us). float32 has no registers for 16 rows.
 //   Warps: as many as leave the registers for a tile of K and of V in flight (d 64, 8 rows: 12 warps 51 us, 16 warps
 //   of fewer registers 57 us; 16 rows: 12 warps 36 us, 8 warps 40 us. d 128, 16 rows: 8 warps 58 us, 10 spill, 96 us).
 //   Where there is little to read, 8: fewer parts to join, no spills (d 128, 4 kv heads: 1000 keys 13.1 us with 12
 //   warps, 11.7 with 8; 32768 keys, 55 units an SM, 23.9 and 22.5; 2 x 60000 keys, 203, 50.0 and 49.8; 8 x 131071, 1771,
-//   322 and 330. float32, d 64, 4 kv heads: 27 units 17.6 and 16.7; 55, 27.4 and 27.9; 101, 38.5 and 41.6).
-constexpr int64_t kFewBf16 = 400, kFewF32 = 40;
+//   322 and 330. float32, d 64, 4 kv heads: 27 units 17.6 and 16.7; 55, 27.4 and 27.9; 101, 38.5 and 41.6). A list of pages
+//   is one more load to wait for, which more warps hide (select and decode of 200 pages of 16 positions, 4 kv heads: 43
+//   units 43.6 us with 12 warps, 42.4 with 8; 86, 60.1 and 59.8; 173, 84 and 89).
+constexpr int64_t kFewBf16 = 400, kFewBf16Listed = 80, kFewF32 = 40;
 
 template <typename F>
-auto with_variant(const PagedMeta& m, int64_t units, F&& fn) {
+auto with_variant(const PagedMeta& m, int64_t units, bool listed, F&& fn) {
     using B = __nv_bfloat16;
     if (m.dtype == SPLITKV_F32) {
         if (m.d > 64) return fn(Variant<float, 128, 1, 8>{});
@@ -861,13 +864,13 @@ auto with_variant(const PagedMeta& m, int64_t units, F&& fn) {
     }
     if (m.group > 8) return m.d <= 64 ? fn(Variant<B, 64, 2, 12>{}) : fn(Variant<B, 128, 2, 8>{});
     if (m.d <= 64) return fn(Variant<B, 64, 1, 12>{});
-    return units <= kFewBf16 ? fn(Variant<B, 128, 1, 8>{}) : fn(Variant<B, 128, 1, 12>{});
+    return units <= (listed ? kFewBf16Listed : kFewBf16) ? fn(Variant<B, 128, 1, 8>{}) : fn(Variant<B, 128, 1, 12>{});
 }
 
 }  // namespace
 
 size_t paged_decode_workspace(const PagedMeta& m) {
-    return with_variant(m, 0, [](auto v) { return decltype(v)::kWorkspace; });
+    return with_variant(m, 0, false, [](auto v) { return decltype(v)::kWorkspace; });
 }
 
 cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,
@@ -879,7 +882,7 @@ cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_str
     if (e != cudaSuccess) return e;
     const int64_t positions = (int64_t)(pages ? std::min(n_select, m.max_pages) : m.max_pages) * m.page;
     const int64_t rows = (int64_t)m.n_seqs * m.hkv * ((m.group + 7) / 8);
-    return with_variant(m, rows * ((positions + kTile - 1) / kTile) / sms, [&](auto v) {
+    return with_variant(m, rows * ((positions + kTile - 1) / kTile) / sms, pages != nullptr, [&](auto v) {
         using V = decltype(v);
         using T = typename V::T;
         auto kern = decode_kernel<T, V::DP, V::NT, V::W>;

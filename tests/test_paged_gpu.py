@@ -226,6 +226,23 @@ def test_decode_offsets_past_32_bits():
     kv.check_status()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64), (16, 4, 112), (4, 4, 40)])
+def test_decode_wide_tables(dtype, hq, hkv, d):
+    # A table for sequences of up to 32768 keys: the launch is made for much to read, whatever the lengths are.
+    c = Case(EDGE_LENS + [5000], hq, hkv, d, 16, dtype, width=2048)
+    o, lse = c.kv.decode(c.q, c.table, c.lens)
+    ref = c.oracle()
+    c.check(o, lse, ref)
+    # So for lists: every page of every sequence, in lists of 2048.
+    lists = np.full((len(c.lens_l), hkv, 2048), -1, dtype=np.int32)
+    for b, n in enumerate(c.lens_l):
+        lists[b, :, :-(-n // 16)] = np.arange(-(-n // 16))
+    o, lse = c.kv.decode(c.q, c.table, c.lens, pages=torch.tensor(lists).cuda())
+    c.check(o, lse, ref)
+    c.kv.check_status()
+
+
 # ------------------------------------------------------------------ decode over listed pages
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("page", [4, 16, 32])
