@@ -521,6 +521,49 @@ def test_select_ties_and_long_rows(count, n_select):
             assert got[b, h, :len(want)].tolist() == want.tolist() and (got[b, h, len(want):] == -1).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n_seqs,count,n_select", [(100, 6000, 50), (1, 131072, 1000), (90, 700, 699)])
+def test_select_many_rows_and_the_longest(dtype, n_seqs, count, n_select):
+    g = torch.Generator().manual_seed(count)
+    d, hkv, hq = 16, 2, 6
+    kb = torch.randn(count + 1, hkv, 2, d, generator=g).sort(2).values.to(dtype).cuda()
+    k = torch.zeros(count + 1, hkv, 1, d, dtype=dtype, device="cuda")
+    q = torch.randn(n_seqs, hq, d, generator=g).to(dtype).cuda()
+    table = torch.stack([torch.randperm(count + 1, generator=g)[:count] for _ in range(n_seqs)]).to(torch.int32).cuda()
+    lens = torch.randint(0, count + 1, (n_seqs,), generator=g, dtype=torch.int32)
+    lens[0] = count
+    kv = PagedKV(hq, hkv, d, 1, max_seqs=n_seqs, max_pages=count, k_cache=k, v_cache=torch.zeros_like(k), k_bounds=kb)
+    got = kv.select(q, table, lens.cuda(), n_select, keep_first=1, keep_last=2).cpu().numpy()
+    kv.check_status()
+    qn, bn, tn = f64(q), f64(kb), table.cpu().numpy()
+    for b in range(n_seqs):
+        n = int(lens[b])
+        for h in range(hkv):
+            qg = qn[b, 3 * h : 3 * h + 3]
+            up, down = np.maximum(qg, 0).sum(0), np.minimum(qg, 0).sum(0)
+            s = bn[tn[b, :n], h, 1] @ up + bn[tn[b, :n], h, 0] @ down
+            s[:1], s[max(n - 2, 0):] = np.inf, np.inf
+            want = np.sort(np.argsort(-s, kind="stable")[:n_select])
+            assert got[b, h, :len(want)].tolist() == want.tolist() and (got[b, h, len(want):] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_most_sequences(dtype):
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 40, B.PAGED_MAX_SEQS).tolist()
+    run_append([n + 1 for n in lens], [1] * len(lens), 4, 2, 16, 4, dtype, 16, False)
+    c = Case(lens, 4, 2, 16, 4, dtype)
+    c.check(*c.kv.decode(c.q, c.table, c.lens), c.oracle())
+    c.kv.check_status()
+    kb = torch.randn(c.k.shape[0], 2, 2, 16, generator=torch.Generator().manual_seed(2)).sort(2).values.to(dtype).cuda()
+    kv = PagedKV(4, 2, 16, 4, max_seqs=len(lens), max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    pages = kv.select(c.q, c.table, c.lens, 3)
+    want = OP.select(f64(c.q), f64(kb), c.table.cpu().numpy(), lens, 4, 3, 1, 1)
+    assert np.array_equal(pages.cpu().numpy(), want)
+    c.check(*kv.decode(c.q, c.table, c.lens, pages=pages), c.oracle(pages=want))
+    kv.check_status()
+
+
 def test_select_far_scores_and_nan():
     # Scores over the whole range of exponents; a NaN score ranks below all. The score is sum_i a_i kmax_i + b_i kmin_i
     # with b_i = 0 here, so an infinite bound gives 0 * inf = NaN too; pages of equal (lowest) rank go by their index.
