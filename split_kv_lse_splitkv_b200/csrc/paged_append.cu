@@ -1,6 +1,6 @@
 // Keys and values of new tokens into a paged cache, rotary positions applied on the way.
 //
-// One launch, bound by the bytes of the rows in and out. A lane holds two 16-byte pieces of a row whose channels are each
+// Bound by the bytes of the rows in and out. A lane holds two pieces (16 bytes) of a row whose channels are each
 // other's partners in the rotation, so it rotates them in registers; a warp takes several rows at once. The new keys
 // of a page and the bounds over the keys it holds are one block's work (the first token of the call in that page has
 // it): the block that rounds a key also has it for the minimum and maximum, keys that were there are read back, and no
@@ -118,27 +118,32 @@ __global__ void __launch_bounds__(128) append_bounds_kernel(PagedMeta m, AppendA
     }
 }
 
-// ---- rope_dim / 2 a multiple of 16 bytes: pieces of 16 bytes
+// ---- pieces of 16 bytes, or of 8: half of rope_dim has to be whole pieces
 
-template <typename T>
-struct Vec;
+// What is loaded and stored as one, and arithmetic on it.
+__device__ __forceinline__ void load_if(uint4& x, const void* p, bool in) { x = ldg_stream_if(p, in); }
+__device__ __forceinline__ void load_if(uint2& x, const void* p, bool in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
+        : "=&r"(x.x), "=&r"(x.y)
+        : "l"(p), "r"((int)in));
+}
+template <typename Type>
+struct Word;  // 32 bits
 template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int kN = 8;
-    static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[8]) {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+struct Word<__nv_bfloat16> {
+    static constexpr int kN = 2;
+    static __device__ __forceinline__ void unpack(uint32_t w, float* f) {
+        f[0] = __uint_as_float(w << 16);
+        f[1] = __uint_as_float(w & 0xffff0000u);
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-        return make_uint4(w[0], w[1], w[2], w[3]);
+    static __device__ __forceinline__ uint32_t pack(const float* f) {
+        uint32_t w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(f[1]), "f"(f[0]));
+        return w;
     }
     template <bool kMax>
     static __device__ __forceinline__ uint32_t best(uint32_t x, uint32_t y) {
@@ -149,14 +154,10 @@ struct Vec<__nv_bfloat16> {
     static constexpr uint32_t kInf = 0x7f807f80u, kNegInf = 0xff80ff80u;
 };
 template <>
-struct Vec<float> {
-    static constexpr int kN = 4;
-    static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[4]) {
-        f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
-    }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    }
+struct Word<float> {
+    static constexpr int kN = 1;
+    static __device__ __forceinline__ void unpack(uint32_t w, float* f) { f[0] = __uint_as_float(w); }
+    static __device__ __forceinline__ uint32_t pack(const float* f) { return __float_as_uint(f[0]); }
     template <bool kMax>
     static __device__ __forceinline__ uint32_t best(uint32_t x, uint32_t y) {
         const float u = __uint_as_float(x), v = __uint_as_float(y);
@@ -164,13 +165,39 @@ struct Vec<float> {
     }
     static constexpr uint32_t kInf = 0x7f800000u, kNegInf = 0xff800000u;
 };
+__device__ __forceinline__ uint32_t& word(uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
+__device__ __forceinline__ uint32_t& word(uint2& x, int i) { return i == 0 ? x.x : x.y; }
+__device__ __forceinline__ uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
+__device__ __forceinline__ uint32_t word(const uint2& x, int i) { return i == 0 ? x.x : x.y; }
 
-template <typename T, bool kMax>
-__device__ __forceinline__ void take(uint4& x, const uint4& y) {
-    x.x = Vec<T>::template best<kMax>(x.x, y.x);
-    x.y = Vec<T>::template best<kMax>(x.y, y.y);
-    x.z = Vec<T>::template best<kMax>(x.z, y.z);
-    x.w = Vec<T>::template best<kMax>(x.w, y.w);
+template <typename Type, typename Of>
+struct Vec {
+    using T = Type;
+    using Piece = Of;
+    using W = Word<T>;
+    static constexpr int kWords = sizeof(Piece) / 4, kN = kWords * W::kN;
+    static __device__ __forceinline__ void unpack(const Piece& x, float (&f)[kN]) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) W::unpack(word(x, i), f + i * W::kN);
+    }
+    static __device__ __forceinline__ Piece pack(const float (&f)[kN]) {
+        Piece x;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) word(x, i) = W::pack(f + i * W::kN);
+        return x;
+    }
+    static __device__ __forceinline__ Piece all(uint32_t w) {
+        Piece x;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) word(x, i) = w;
+        return x;
+    }
+};
+
+template <typename V, bool kMax>
+__device__ __forceinline__ void take(typename V::Piece& x, const typename V::Piece& y) {
+#pragma unroll
+    for (int i = 0; i < V::kWords; ++i) word(x, i) = V::W::template best<kMax>(word(x, i), word(y, i));
 }
 
 // How a row of d channels lies over lanes: `per_row` lanes a row, two pieces a lane.
@@ -180,9 +207,9 @@ struct Lanes {
     int pair;           // first angle of its pairs, or -1: not rotated
 };
 
-template <typename T>
+template <typename V>
 __device__ __forceinline__ Lanes lanes_of(int d, int rope_dim, int interleaved, int lane) {
-    constexpr int kN = Vec<T>::kN;
+    constexpr int kN = V::kN;
     const int turned = rope_dim / 2 / kN, rest = (d - rope_dim) / kN;
     Lanes x;
     x.per_row = turned + (rest + 1) / 2;
@@ -201,24 +228,31 @@ __device__ __forceinline__ Lanes lanes_of(int d, int rope_dim, int interleaved, 
     return x;
 }
 
-template <typename T>
+template <typename V>
 struct Angles {
-    float c[Vec<T>::kN], s[Vec<T>::kN];
+    using Piece = typename V::Piece;
+    float c[V::kN], s[V::kN];
     __device__ __forceinline__ void load(const float* row, int half, int pair) {
 #pragma unroll
-        for (int i = 0; i < Vec<T>::kN; i += 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(row + pair + i));
-            const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + pair + i));
-            c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-            s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+        for (int i = 0; i < V::kN; i += 4) {
+            if constexpr (V::kN >= 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(row + pair + i));
+                const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + pair + i));
+                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+                s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+            } else {
+                const float2 x = __ldg(reinterpret_cast<const float2*>(row + pair));
+                const float2 y = __ldg(reinterpret_cast<const float2*>(row + half + pair));
+                c[0] = x.x, c[1] = x.y, s[0] = y.x, s[1] = y.y;
+            }
         }
     }
     // (x c - y s, y c + x s) for each pair (x, y), in float32, rounded once to the type.
-    __device__ __forceinline__ void turn(uint4& a, uint4& b, int interleaved) const {
-        constexpr int kN = Vec<T>::kN;
+    __device__ __forceinline__ void turn(Piece& a, Piece& b, int interleaved) const {
+        constexpr int kN = V::kN;
         float x[kN], y[kN], u[kN], w[kN];
-        Vec<T>::unpack(a, x);
-        Vec<T>::unpack(b, y);
+        V::unpack(a, x);
+        V::unpack(b, y);
         if (interleaved) {
 #pragma unroll
             for (int i = 0; i < kN / 2; ++i) {
@@ -234,49 +268,52 @@ struct Angles {
                 w[i] = fmaf(y[i], c[i], x[i] * s[i]);
             }
         }
-        a = Vec<T>::pack(u);
-        b = Vec<T>::pack(w);
+        a = V::pack(u);
+        b = V::pack(w);
     }
 };
 
 // kAhead rows a lane: rows (heads) h, h + L.rows, .. below h1.
-template <typename T, int kAhead>
+template <typename V, int kAhead>
 struct Rows {
-    uint4 x[kAhead], y[kAhead];
+    using T = typename V::T;
+    using Piece = typename V::Piece;
+    Piece x[kAhead], y[kAhead];
     __device__ __forceinline__ void load(const PagedMeta& m, const Lanes& L, const T* src, int h, int h1) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int64_t at = (int64_t)(h + k * L.rows) * m.d;
             const bool in = L.row < L.rows && h + k * L.rows < h1;
-            x[k] = ldg_stream_if(src + at + L.a, in);
-            y[k] = ldg_stream_if(src + at + L.b, in && L.b >= 0);
+            load_if(x[k], src + at + L.a, in);
+            load_if(y[k], src + at + L.b, in && L.b >= 0);
         }
     }
     __device__ __forceinline__ void store(const AppendArgs& a, const Lanes& L, T* dst, int64_t step, int h, int h1,
-                                          const Angles<T>* turn) {
+                                          const Angles<V>* turn) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (L.row >= L.rows || h + k * L.rows >= h1) continue;
             if (turn) turn->turn(x[k], y[k], a.interleaved);
             T* row = dst + (h + k * L.rows) * step;
-            *reinterpret_cast<uint4*>(row + L.a) = x[k];
-            if (L.b >= 0) *reinterpret_cast<uint4*>(row + L.b) = y[k];
+            *reinterpret_cast<Piece*>(row + L.a) = x[k];
+            if (L.b >= 0) *reinterpret_cast<Piece*>(row + L.b) = y[k];
         }
     }
 };
 
 // Queries of one token, heads [h0, h1), on a warp. The first rows are asked for before the token's position is known.
-template <typename T, int kAhead>
+template <typename V, int kAhead>
 __device__ __forceinline__ void append_queries(const PagedMeta& m, const AppendArgs& a, int64_t i, int h0, int h1,
                                                int lane) {
-    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    using T = typename V::T;
+    const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
     const T* src = (const T*)a.q + i * a.q_stride;
-    Rows<T, kAhead> r;
+    Rows<V, kAhead> r;
     r.load(m, L, src, h0 + L.row, h1);
     const int32_t seq = __ldg(a.token_seq + i), pos = __ldg(a.token_pos + i);
     // A token that is out of range is reported with its keys; its queries pass as they are.
     const bool turn = L.pair >= 0 && seq >= 0 && pos >= 0 && pos < a.rope_len;
-    Angles<T> ang;
+    Angles<V> ang;
     if (turn) ang.load(a.rope + (int64_t)pos * a.rope_dim, a.rope_dim / 2, L.pair);
     for (int h = h0;;) {
         r.store(a, L, (T*)a.q_out + i * m.hq * m.d, m.d, h + L.row, h1, turn ? &ang : nullptr);
@@ -329,12 +366,14 @@ struct Units {
     __host__ __device__ int64_t of(int64_t n) const { return (n + tokens - 1) / tokens * per_token; }
 };
 
-template <typename T>
+template <typename V>
 __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+    using T = typename V::T;
+    using Piece = typename V::Piece;
     after_previous();
     if (status_bad(status)) return;
     const int lane = threadIdx.x & 31;
-    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
     const Units Q(m.hq, 4 * L.rows), KV(m.hkv, 2 * L.rows);
     int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5);
     const int64_t q_units = a.q ? Q.of(a.n_tokens) : 0;
@@ -349,11 +388,11 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
         i = i0 + t, h = h0 + x - t * U.heads;
         return L.row < L.rows && t < U.tokens && i < a.n_tokens && h < (queries ? m.hq : m.hkv);
     };
-    Angles<T> ang;
+    Angles<V> ang;
     int64_t i[2];
     int32_t h[2];
     bool in[2];
-    uint4 x[2], y[2];
+    Piece x[2], y[2];
     if (queries) {
         int64_t now = -1;  // the token whose angles are at hand
         bool turn = false;
@@ -362,8 +401,8 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
             for (int k = 0; k < 2; ++k) {
                 in[k] = row(step + k, i[k], h[k]);
                 const T* src = (const T*)a.q + i[k] * a.q_stride + (int64_t)h[k] * m.d;
-                x[k] = ldg_stream_if(src + L.a, in[k]);
-                y[k] = ldg_stream_if(src + L.b, in[k] && L.b >= 0);
+                load_if(x[k], src + L.a, in[k]);
+                load_if(y[k], src + L.b, in[k] && L.b >= 0);
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -377,22 +416,22 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
                 }
                 if (turn) ang.turn(x[k], y[k], a.interleaved);
                 T* dst = (T*)a.q_out + (i[k] * m.hq + h[k]) * m.d;
-                *reinterpret_cast<uint4*>(dst + L.a) = x[k];
-                if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = y[k];
+                *reinterpret_cast<Piece*>(dst + L.a) = x[k];
+                if (L.b >= 0) *reinterpret_cast<Piece*>(dst + L.b) = y[k];
             }
         }
         return;
     }
-    uint4 z[2], w[2];
+    Piece z[2], w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         in[k] = row(k, i[k], h[k]);
         const T* src = (const T*)a.k + i[k] * a.k_stride + (int64_t)h[k] * m.d;
-        x[k] = ldg_stream_if(src + L.a, in[k]);
-        y[k] = ldg_stream_if(src + L.b, in[k] && L.b >= 0);
+        load_if(x[k], src + L.a, in[k]);
+        load_if(y[k], src + L.b, in[k] && L.b >= 0);
         src = (const T*)a.v + i[k] * a.v_stride + (int64_t)h[k] * m.d;
-        z[k] = ldg_stream_if(src + L.a, in[k]);
-        w[k] = ldg_stream_if(src + L.b, in[k] && L.b >= 0);
+        load_if(z[k], src + L.a, in[k]);
+        load_if(w[k], src + L.b, in[k] && L.b >= 0);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -405,11 +444,11 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
         }
         const int64_t at = paged_row(m, t.page, h[k], t.pos & (m.page - 1));
         T* dst = (T*)a.k_cache + at;
-        *reinterpret_cast<uint4*>(dst + L.a) = x[k];
-        if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = y[k];
+        *reinterpret_cast<Piece*>(dst + L.a) = x[k];
+        if (L.b >= 0) *reinterpret_cast<Piece*>(dst + L.b) = y[k];
         dst = (T*)a.v_cache + at;
-        *reinterpret_cast<uint4*>(dst + L.a) = z[k];
-        if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = w[k];
+        *reinterpret_cast<Piece*>(dst + L.a) = z[k];
+        if (L.b >= 0) *reinterpret_cast<Piece*>(dst + L.b) = w[k];
     }
 }
 
@@ -423,10 +462,11 @@ __global__ void __launch_bounds__(kStreamThreads) append_order_kernel(PagedMeta 
 // Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's 32, at one kv head.
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+    using V = Vec<T, uint4>;
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * 32;
     const int32_t g = (int32_t)(unit % m.hkv);
-    const Lanes L = lanes_of<T>(m.d, 0, 0, lane);
+    const Lanes L = lanes_of<V>(m.d, 0, 0, lane);
     uint32_t firsts = page_firsts(m, a, i0, 32, lane, g == 0, status);
     bool waited = false;
     if (!firsts) after_previous();
@@ -456,8 +496,8 @@ __global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel
         uint4 lo[2], hi[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            lo[x] = make_uint4(Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf);
-            hi[x] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
+            lo[x] = V::all(V::W::kInf);
+            hi[x] = V::all(V::W::kNegInf);
         }
         const T* kc = (const T*)a.k_cache + paged_row(m, page, g, 0);
         constexpr int kAhead = 4;
@@ -473,8 +513,8 @@ __global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (L.row >= L.rows || off0 + u * L.rows + L.row > last) continue;
-                take<T, false>(lo[0], x[u]), take<T, true>(hi[0], x[u]);
-                take<T, false>(lo[1], y[u]), take<T, true>(hi[1], y[u]);
+                take<V, false>(lo[0], x[u]), take<V, true>(hi[0], x[u]);
+                take<V, false>(lo[1], y[u]), take<V, true>(hi[1], y[u]);
             }
         }
         for (int r = 1; r < L.rows; ++r) {  // the lanes of the first row take the others'
@@ -486,7 +526,7 @@ __global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const uint4 l = from(lo[x]), h = from(hi[x]);
-                if (lane < L.per_row) take<T, false>(lo[x], l), take<T, true>(hi[x], h);
+                if (lane < L.per_row) take<V, false>(lo[x], l), take<V, true>(hi[x], h);
             }
         }
         if (L.row == 0) {
@@ -503,15 +543,17 @@ __global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel
 
 // Blocks [0, kv_blocks): the keys and values of the pages whose first token of the call is one of the block's
 // `slice` tokens, and the pages' bounds. Blocks from there on: queries, `heads` of a token per warp.
-template <typename T>
+template <typename V>
 __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArgs a, int32_t* status, int64_t kv_blocks,
                                                           int32_t slice, int32_t heads) {
-    constexpr int kN = Vec<T>::kN;
+    using T = typename V::T;
+    using Piece = typename V::Piece;
+    constexpr int kN = Vec<T, uint4>::kN;  // of values: they are not turned
     __shared__ int32_t tokens[kMaxPage];      // the page's new tokens, from the first one on,
     __shared__ uint16_t offs[kMaxPage];       // and where in the page they go
     __shared__ uint32_t is_new[kMaxPage / 32];
     __shared__ int32_t n_tokens, last_pos;
-    __shared__ uint4 red[kWarps][32][4];      // minima and maxima of a lane's two pieces
+    __shared__ Piece red[kWarps][32][4];      // minima and maxima of a lane's two pieces
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     after_previous();
     if (__syncthreads_or(status_bad(status))) return;
@@ -520,11 +562,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
         const int32_t per_token = (m.hq + heads - 1) / heads;
         const int64_t unit = (blockIdx.x - kv_blocks) * kWarps + warp, i = unit / per_token;
         const int32_t h0 = (int32_t)(unit - i * per_token) * heads;
-        if (i < a.n_tokens) append_queries<T, 4>(m, a, i, h0, min(h0 + heads, m.hq), lane);
+        if (i < a.n_tokens) append_queries<V, 4>(m, a, i, h0, min(h0 + heads, m.hq), lane);
         return;
     }
 
-    const Lanes L = lanes_of<T>(m.d, a.rope_dim, a.interleaved, lane);
+    const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
     const int v_row = m.d / kN, v_rows = 32 / v_row;  // values: a lane per piece
     // Which of the slice's tokens are the first of a page: a lane per token, the same in every warp.
     const int64_t i0 = blockIdx.x * (int64_t)slice;
@@ -571,11 +613,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
         for (int32_t task0 = 0; task0 < m.hkv * subs; task0 += kWarps) {
             const int32_t task = task0 + warp, g = task / subs, sub = task - g * subs;
             const bool work = task < m.hkv * subs;
-            uint4 lo[2], hi[2];
+            Piece lo[2], hi[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                lo[x] = make_uint4(Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf, Vec<T>::kInf);
-                hi[x] = make_uint4(Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf, Vec<T>::kNegInf);
+                lo[x] = V::all(V::W::kInf);
+                hi[x] = V::all(V::W::kNegInf);
             }
             T* kc = (T*)a.k_cache + paged_row(m, page, work ? g : 0, 0);
             T* vc = (T*)a.v_cache + paged_row(m, page, work ? g : 0, 0);
@@ -583,21 +625,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
             if (work && L.row < L.rows && a.k_bounds) {  // keys that were there
                 constexpr int kAhead = 4;
                 for (int32_t off = sub * L.rows + L.row; off < last; off += kAhead * subs * L.rows) {
-                    uint4 x[kAhead], y[kAhead];
+                    Piece x[kAhead], y[kAhead];
                     bool in[kAhead];
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) {
                         const int32_t at = off + u * subs * L.rows;
                         in[u] = at < last && !(is_new[at >> 5] >> (at & 31) & 1);
                         const T* src = kc + at * m.token_stride;
-                        x[u] = ldg_stream_if(src + L.a, in[u]);
-                        y[u] = ldg_stream_if(src + L.b, in[u] && L.b >= 0);
+                        load_if(x[u], src + L.a, in[u]);
+                        load_if(y[u], src + L.b, in[u] && L.b >= 0);
                     }
 #pragma unroll
                     for (int u = 0; u < kAhead; ++u) {
                         if (!in[u]) continue;
-                        take<T, false>(lo[0], x[u]), take<T, true>(hi[0], x[u]);
-                        take<T, false>(lo[1], y[u]), take<T, true>(hi[1], y[u]);  // (not used where there is no second piece)
+                        take<V, false>(lo[0], x[u]), take<V, true>(hi[0], x[u]);
+                        take<V, false>(lo[1], y[u]), take<V, true>(hi[1], y[u]);  // (not used where there is no second piece)
                     }
                 }
             }
@@ -607,8 +649,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
             int32_t k0 = work && L.row < L.rows ? sub * L.rows + L.row : n;
             int32_t v0 = work && lane < v_rows * v_row ? sub * v_rows + lane / v_row : n;
             for (; k0 < n || v0 < n; k0 += steps, v0 += v_steps) {
-                uint4 x[kKeys], y[kKeys], z[kValues];
-                Angles<T> ang[kKeys];
+                Piece x[kKeys], y[kKeys];
+                uint4 z[kValues];
+                Angles<V> ang[kKeys];
                 int32_t off[kKeys];
 #pragma unroll
                 for (int u = 0; u < kKeys; ++u) {
@@ -616,8 +659,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
                     const bool in = at < n;
                     off[u] = in ? offs[at] : -1;
                     const T* src = (const T*)a.k + (i + (in ? tokens[at] : 0)) * a.k_stride + g * m.d;
-                    x[u] = ldg_stream_if(src + L.a, in);
-                    y[u] = ldg_stream_if(src + L.b, in && L.b >= 0);
+                    load_if(x[u], src + L.a, in);
+                    load_if(y[u], src + L.b, in && L.b >= 0);
                 }
 #pragma unroll
                 for (int u = 0; u < kValues; ++u) {
@@ -633,10 +676,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
                     if (off[u] < 0) continue;
                     if (L.pair >= 0) ang[u].turn(x[u], y[u], a.interleaved);
                     T* dst = kc + off[u] * m.token_stride;
-                    *reinterpret_cast<uint4*>(dst + L.a) = x[u];
-                    if (L.b >= 0) *reinterpret_cast<uint4*>(dst + L.b) = y[u];
-                    take<T, false>(lo[0], x[u]), take<T, true>(hi[0], x[u]);
-                    take<T, false>(lo[1], y[u]), take<T, true>(hi[1], y[u]);
+                    *reinterpret_cast<Piece*>(dst + L.a) = x[u];
+                    if (L.b >= 0) *reinterpret_cast<Piece*>(dst + L.b) = y[u];
+                    take<V, false>(lo[0], x[u]), take<V, true>(hi[0], x[u]);
+                    take<V, false>(lo[1], y[u]), take<V, true>(hi[1], y[u]);
                 }
 #pragma unroll
                 for (int u = 0; u < kValues; ++u) {
@@ -653,18 +696,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
                 for (int x = lane; x < 2 * L.per_row; x += 32) {
                     const bool top = x >= L.per_row;
                     const int j = top ? x - L.per_row : x;
-                    const Lanes J = lanes_of<T>(m.d, a.rope_dim, a.interleaved, j);
+                    const Lanes J = lanes_of<V>(m.d, a.rope_dim, a.interleaved, j);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int c = half ? J.b : J.a;
                         if (c < 0) continue;
-                        uint4 best = red[warp][j][half + (top ? 2 : 0)];
+                        Piece best = red[warp][j][half + (top ? 2 : 0)];
                         for (int w = 0; w < warps; ++w)
                             for (int r = 0; r < L.rows; ++r) {
-                                const uint4 y = red[warp + w][r * L.per_row + j][half + (top ? 2 : 0)];
-                                if (top) take<T, true>(best, y); else take<T, false>(best, y);
+                                const Piece y = red[warp + w][r * L.per_row + j][half + (top ? 2 : 0)];
+                                if (top) take<V, true>(best, y); else take<V, false>(best, y);
                             }
-                        *reinterpret_cast<uint4*>((T*)a.k_bounds + (((int64_t)page * m.hkv + g) * 2 + top) * m.d + c) = best;
+                        *reinterpret_cast<Piece*>((T*)a.k_bounds + (((int64_t)page * m.hkv + g) * 2 + top) * m.d + c) = best;
                     }
                 }
             }
@@ -673,18 +716,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArg
     }
 }
 
-template <typename T>
-cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
-    if (a.rope_dim / 2 % Vec<T>::kN) {
-        append_rows_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
-        if (a.k_bounds) append_bounds_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
-        return note_error(cudaGetLastError(), "paged append");
-    }
+template <typename V>
+cudaError_t launch_pieces(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
+    using T = typename V::T;
     constexpr int kSms = 148;
     // A block per token while there are few; then as many tokens a block as leave several blocks per SM.
     const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens / (kSms * 4)));
     const int64_t kv_blocks = (a.n_tokens + slice - 1) / slice;
-    const int turned = a.rope_dim / 2 / Vec<T>::kN, rows = 32 / (turned + ((m.d - a.rope_dim) / Vec<T>::kN + 1) / 2);
+    const int rows = 32 / (a.rope_dim / 2 / V::kN + ((m.d - a.rope_dim) / V::kN + 1) / 2);
     const int64_t all = a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv);
     // From about what the SMs hold at once the rows stream. 32/4 heads, d 128, 500 tokens (5000 warps' rows): pages of 64
     // 8.9 us so and 13.5 page by page, pages of 16 11.4 and 9.6; 2000 tokens 14.0 and 19.1, 16.4 and 20.3; 8000 tokens 37
@@ -692,18 +731,30 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     if (all / rows >= kSms * 32) {
         const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
         const int64_t slices = (a.n_tokens + 31) / 32 * (a.k_bounds ? m.hkv : 1);
-        cudaError_t e = launch_overlapped(append_stream_kernel<T>, (units + kStreamWarps - 1) / kStreamWarps,
+        cudaError_t e = launch_overlapped(append_stream_kernel<V>, (units + kStreamWarps - 1) / kStreamWarps,
                                           kStreamThreads, 0, st, m, a, status);
         if (e == cudaSuccess)
-            e = launch_overlapped(a.k_bounds ? append_bounds_stream_kernel<T> : append_order_kernel, (slices + kStreamWarps - 1) / kStreamWarps,
-                                  kStreamThreads, 0, st, m, a, status);
+            e = launch_overlapped(a.k_bounds ? append_bounds_stream_kernel<T> : append_order_kernel,
+                                  (slices + kStreamWarps - 1) / kStreamWarps, kStreamThreads, 0, st, m, a, status);
         return note_error(e, "paged append");
     }
     const int32_t heads = std::min(m.hq, rows);
     const int64_t q_blocks = a.q ? (a.n_tokens * ((m.hq + heads - 1) / heads) + kWarps - 1) / kWarps : 0;
-    return note_error(launch_overlapped(append_kernel<T>, kv_blocks + q_blocks, kThreads, 0, st, m, a, status,
+    return note_error(launch_overlapped(append_kernel<V>, kv_blocks + q_blocks, kThreads, 0, st, m, a, status,
                                         kv_blocks, slice, heads),
                       "paged append");
+}
+
+// 16 bytes a piece where half of rope_dim is a multiple of them, 8 where it is of those (16000 tokens, 32/4 heads, d 80,
+// rope_dim 40 in bf16: 63 us; rope_dim 80, 16 bytes: 53; channel by channel: 196), else channel by channel.
+template <typename T>
+cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
+    const int half = a.rope_dim / 2;
+    if (half % Vec<T, uint4>::kN == 0) return launch_pieces<Vec<T, uint4>>(m, a, status, st);
+    if (half % Vec<T, uint2>::kN == 0) return launch_pieces<Vec<T, uint2>>(m, a, status, st);
+    append_rows_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+    if (a.k_bounds) append_bounds_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+    return note_error(cudaGetLastError(), "paged append");
 }
 
 }  // namespace

@@ -415,6 +415,21 @@ def test_append_order_is_checked_across_padding(run, tokens, rot):
     assert kv.status_value() == B.DEV_TOKEN_ORDER
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hq,hkv,d,rot", [(32, 4, 80, 40), (8, 2, 128, 24), (6, 2, 64, 8), (4, 1, 128, 4), (3, 3, 24, 12),
+                                          (8, 8, 112, 104), (1, 1, 8, 4)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("page", [4, 64])
+def test_append_narrow_rotations(dtype, hq, hkv, d, rot, interleaved, page):
+    # Half of the rotated channels is not a multiple of 16 bytes: pieces of 8, or channel by channel. Few tokens and many.
+    run_append([1, 5, 40, 33, 16, 100], [1, 5, 1, 2, 16, 70], hq, hkv, d, page, dtype, rot, interleaved, padding=(3, 4),
+               seed=d + rot)
+    rows = max(1, 32 // max(1, d * (2 if dtype == BF else 4) // 16))
+    n = 148 * 32 * rows // (hq + 2 * hkv) + 100
+    run_append([n // 2 + 3, 5, n // 2], [n // 2 - 9, 5, n // 2], hq, hkv, d, page, dtype, rot, interleaved,
+               padding=(0, 7, 40, 300), seed=rot)
+
+
 def test_append_many_tokens_orders_and_options():
     run_append([3000, 2000], [2500, 2000], 8, 2, 128, 32, BF, 128, False, order="positions")
     run_append([3000, 2000], [2500, 2000], 8, 2, 128, 32, F32, 128, True, order="gaps")
