@@ -452,22 +452,24 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
     }
 }
 
-// Many tokens without bounds, second launch: what is wrong with the tokens, 32 a warp.
-__global__ void __launch_bounds__(kStreamThreads) append_order_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+// Many tokens without bounds, second launch: what is wrong with the tokens, `slice` a warp.
+__global__ void __launch_bounds__(kStreamThreads) append_order_kernel(PagedMeta m, AppendArgs a, int32_t* status,
+                                                                      int32_t slice) {
     after_previous();
     const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5);
-    page_firsts(m, a, unit * 32, 32, threadIdx.x & 31, true, status);
+    page_firsts(m, a, unit * slice, slice, threadIdx.x & 31, true, status);
 }
 
-// Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's 32, at one kv head.
+// Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's `slice`, at one kv head.
 template <typename T>
-__global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status,
+                                                                                int32_t slice) {
     using V = Vec<T, uint4>;
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * 32;
+    const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * slice;
     const int32_t g = (int32_t)(unit % m.hkv);
     const Lanes L = lanes_of<V>(m.d, 0, 0, lane);
-    uint32_t firsts = page_firsts(m, a, i0, 32, lane, g == 0, status);
+    uint32_t firsts = page_firsts(m, a, i0, slice, lane, g == 0, status);
     bool waited = false;
     if (!firsts) after_previous();
     for (; firsts; firsts &= firsts - 1) {
@@ -730,12 +732,15 @@ cudaError_t launch_pieces(const PagedMeta& m, const AppendArgs& a, int32_t* stat
     // and 66, 37 and 71.
     if (all / rows >= kSms * 32) {
         const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
-        const int64_t slices = (a.n_tokens + 31) / 32 * (a.k_bounds ? m.hkv : 1);
+        // Tokens a warp looks through for pages: few where each may be a page of its own (1000 sequences' tokens, 32/8 heads:
+        // 32 a warp 70 us, so 18), many where there are enough warps.
+        const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens * m.hkv / (kSms * 16)));
+        const int64_t slices = (a.n_tokens + slice - 1) / slice * (a.k_bounds ? m.hkv : 1);
         cudaError_t e = launch_overlapped(append_stream_kernel<V>, (units + kStreamWarps - 1) / kStreamWarps,
                                           kStreamThreads, 0, st, m, a, status);
         if (e == cudaSuccess)
             e = launch_overlapped(a.k_bounds ? append_bounds_stream_kernel<T> : append_order_kernel,
-                                  (slices + kStreamWarps - 1) / kStreamWarps, kStreamThreads, 0, st, m, a, status);
+                                  (slices + kStreamWarps - 1) / kStreamWarps, kStreamThreads, 0, st, m, a, status, slice);
         return note_error(e, "paged append");
     }
     const int32_t heads = std::min(m.hq, rows);
