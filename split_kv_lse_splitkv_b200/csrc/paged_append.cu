@@ -1,10 +1,10 @@
 // Keys and values of new tokens into a paged cache, rotary positions applied on the way.
 //
-// Bound by the bytes of the rows in and out. A lane holds two pieces (16 bytes) of a row whose channels are each
-// other's partners in the rotation, so it rotates them in registers; a warp takes several rows at once. The new keys
-// of a page and the bounds over the keys it holds are one block's work (the first token of the call in that page has
-// it): the block that rounds a key also has it for the minimum and maximum, keys that were there are read back, and no
-// two blocks write one page's bounds.
+// Bound by the bytes of the rows in and out. A lane holds two pieces (16 bytes) of a row whose channels are each other's
+// partners in the rotation, so it rotates them in registers; a warp takes several rows at once. The bounds over the keys of
+// a page that is written are one warp's work (or one block's), the one that finds the call's first token in that page: no
+// two write one page's bounds. Few tokens: rows and bounds in one launch, the new keys turned a second time for their bounds
+// so that nothing waits. Many: rows first, then the bounds from the keys as the cache holds them, in L2.
 #include <math.h>
 
 #include <algorithm>
@@ -14,10 +14,8 @@
 namespace splitkv {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Blocks of the streaming kernels: 128 threads 140 us, 256 143, 512 149 (35k tokens, 32/4 heads).
-constexpr int kStreamThreads = 128, kStreamWarps = kStreamThreads / 32;
-constexpr int kMaxPage = 1024;
+// 128 threads a block 140 us, 256 143, 512 149 (35k tokens, 32/4 heads).
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 
 // Where token i goes. Padding and tokens out of range have page -1; the order is checked against the token
 // before it that is not padding.
@@ -70,7 +68,7 @@ __device__ T rotated(const AppendArgs& a, const T* x, int32_t i, const float* cs
 
 // ---- any rope_dim: channels one by one. One block per token: queries, keys and values.
 template <typename T>
-__global__ void __launch_bounds__(128) append_rows_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__global__ void __launch_bounds__(128) append_channels_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     if (status_bad(status)) return;
     const int64_t i = blockIdx.x;
     const TokenPlace t = token_place(m, a, i, status);
@@ -96,7 +94,7 @@ __global__ void __launch_bounds__(128) append_rows_kernel(PagedMeta m, AppendArg
 
 // One block per token: the bounds of its page, if no later token of the call writes the same page.
 template <typename T>
-__global__ void __launch_bounds__(128) append_bounds_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__global__ void __launch_bounds__(128) append_channels_bounds_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     if (status_bad(status)) return;
     const int64_t i = blockIdx.x;
     const TokenPlace t = token_place(m, a, i, status);
@@ -273,55 +271,6 @@ struct Angles {
     }
 };
 
-// kAhead rows a lane: rows (heads) h, h + L.rows, .. below h1.
-template <typename V, int kAhead>
-struct Rows {
-    using T = typename V::T;
-    using Piece = typename V::Piece;
-    Piece x[kAhead], y[kAhead];
-    __device__ __forceinline__ void load(const PagedMeta& m, const Lanes& L, const T* src, int h, int h1) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int64_t at = (int64_t)(h + k * L.rows) * m.d;
-            const bool in = L.row < L.rows && h + k * L.rows < h1;
-            load_if(x[k], src + at + L.a, in);
-            load_if(y[k], src + at + L.b, in && L.b >= 0);
-        }
-    }
-    __device__ __forceinline__ void store(const AppendArgs& a, const Lanes& L, T* dst, int64_t step, int h, int h1,
-                                          const Angles<V>* turn) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (L.row >= L.rows || h + k * L.rows >= h1) continue;
-            if (turn) turn->turn(x[k], y[k], a.interleaved);
-            T* row = dst + (h + k * L.rows) * step;
-            *reinterpret_cast<Piece*>(row + L.a) = x[k];
-            if (L.b >= 0) *reinterpret_cast<Piece*>(row + L.b) = y[k];
-        }
-    }
-};
-
-// Queries of one token, heads [h0, h1), on a warp. The first rows are asked for before the token's position is known.
-template <typename V, int kAhead>
-__device__ __forceinline__ void append_queries(const PagedMeta& m, const AppendArgs& a, int64_t i, int h0, int h1,
-                                               int lane) {
-    using T = typename V::T;
-    const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
-    const T* src = (const T*)a.q + i * a.q_stride;
-    Rows<V, kAhead> r;
-    r.load(m, L, src, h0 + L.row, h1);
-    const int32_t seq = __ldg(a.token_seq + i), pos = __ldg(a.token_pos + i);
-    // A token that is out of range is reported with its keys; its queries pass as they are.
-    const bool turn = L.pair >= 0 && seq >= 0 && pos >= 0 && pos < a.rope_len;
-    Angles<V> ang;
-    if (turn) ang.load(a.rope + (int64_t)pos * a.rope_dim, a.rope_dim / 2, L.pair);
-    for (int h = h0;;) {
-        r.store(a, L, (T*)a.q_out + i * m.hq * m.d, m.d, h + L.row, h1, turn ? &ang : nullptr);
-        if ((h += kAhead * L.rows) >= h1) break;
-        r.load(m, L, src, h + L.row, h1);
-    }
-}
-
 // Which of the `slice` <= 32 tokens from i0 on (a lane each) are the first of the call in their page. `report`: say what is
 // wrong with them, their order included, in the status word.
 __device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const AppendArgs& a, int64_t i0, int32_t slice,
@@ -353,11 +302,8 @@ __device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const Append
     return __ballot_sync(0xffffffffu, first);
 }
 
-// Many tokens: rows by themselves. A unit is `most` rows: that many heads of one token, or all heads of several tokens
-// where they are few. A warp has a unit of queries, or one of keys and the same one of values. What is wrong with
-// the tokens' order is found, and the bounds of the keys are taken, in a launch of its own, from L2 (looking at the order
-// beside the rows costs 4 us of 140). (A page's rows and bounds in one block, as below, keep too few loads in
-// flight to fill the GPU: 35k tokens took 52 us for keys and values alone, against 23 us for their bytes.)
+// Rows by themselves. A unit is `most` rows: that many heads of one token, or all heads of several tokens where they are
+// few. A warp has a unit of queries, or one of keys and the same one of values.
 struct Units {
     int32_t heads, tokens;  // of a unit
     int32_t per_token;      // units that a token's heads take
@@ -367,15 +313,11 @@ struct Units {
 };
 
 template <typename V>
-__global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
+__device__ __forceinline__ void append_rows(const PagedMeta& m, const AppendArgs& a, int64_t unit, int lane, int32_t* status) {
     using T = typename V::T;
     using Piece = typename V::Piece;
-    after_previous();
-    if (status_bad(status)) return;
-    const int lane = threadIdx.x & 31;
     const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
     const Units Q(m.hq, 4 * L.rows), KV(m.hkv, 2 * L.rows);
-    int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5);
     const int64_t q_units = a.q ? Q.of(a.n_tokens) : 0;
     const bool queries = unit < q_units;
     const Units U = queries ? Q : KV;
@@ -452,25 +394,29 @@ __global__ void __launch_bounds__(kStreamThreads, 8) append_stream_kernel(PagedM
     }
 }
 
-// Many tokens without bounds, second launch: what is wrong with the tokens, `slice` a warp.
-__global__ void __launch_bounds__(kStreamThreads) append_order_kernel(PagedMeta m, AppendArgs a, int32_t* status,
-                                                                      int32_t slice) {
+// Many tokens, first launch: rows. (With the bounds in the same launch, the registers they take cost the rows' loads in
+// flight: 35k tokens 144 to 165 us in one launch, 140 in two.)
+template <typename V>
+__global__ void __launch_bounds__(kThreads, 8) append_rows_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
     after_previous();
-    const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5);
-    page_firsts(m, a, unit * slice, slice, threadIdx.x & 31, true, status);
+    if (status_bad(status)) return;
+    append_rows<V>(m, a, (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), threadIdx.x & 31, status);
 }
 
-// Many tokens, second launch: the bounds of the pages whose first token of the call is among a warp's `slice`, at one kv head.
+// Second launch: what is wrong with the tokens' order (looking at it beside the rows costs 4 us of 140), and, at one kv
+// head, the bounds of the pages whose first token of the call is among a warp's `slice`, from L2.
 template <typename T>
-__global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel(PagedMeta m, AppendArgs a, int32_t* status,
+__global__ void __launch_bounds__(kThreads, 7) append_bounds_kernel(PagedMeta m, AppendArgs a, int32_t* status,
                                                                                 int32_t slice) {
     using V = Vec<T, uint4>;
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kStreamWarps + (threadIdx.x >> 5), i0 = unit / m.hkv * slice;
-    const int32_t g = (int32_t)(unit % m.hkv);
+    const int32_t heads = a.k_bounds ? m.hkv : 1;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), i0 = unit / heads * slice;
+    const int32_t g = (int32_t)(unit % heads);
     const Lanes L = lanes_of<V>(m.d, 0, 0, lane);
     uint32_t firsts = page_firsts(m, a, i0, slice, lane, g == 0, status);
     bool waited = false;
+    if (!a.k_bounds) firsts = 0;
     if (!firsts) after_previous();
     for (; firsts; firsts &= firsts - 1) {
         const int64_t i = i0 + __ffs(firsts) - 1;
@@ -543,178 +489,155 @@ __global__ void __launch_bounds__(kStreamThreads, 7) append_bounds_stream_kernel
     }
 }
 
-// Blocks [0, kv_blocks): the keys and values of the pages whose first token of the call is one of the block's
-// `slice` tokens, and the pages' bounds. Blocks from there on: queries, `heads` of a token per warp.
+// Few tokens, one launch. The bounds of page `page` at kv head g, its new tokens the call's from i on, on the warps of a block that share it (`split`
+// of them, this one `sub`; all of them come here together) or on one. New keys are turned once more: so nothing waits for the
+// rows to be written, and the keys are in L2 twice in a row.
 template <typename V>
-__global__ void __launch_bounds__(kThreads) append_kernel(PagedMeta m, AppendArgs a, int32_t* status, int64_t kv_blocks,
-                                                          int32_t slice, int32_t heads) {
+__device__ __forceinline__ void page_bounds(const PagedMeta& m, const AppendArgs& a, int64_t i, int32_t page, int32_t g,
+                                            int32_t split, int32_t sub, int lane, typename V::Piece (*red)[32][4]) {
     using T = typename V::T;
     using Piece = typename V::Piece;
-    constexpr int kN = Vec<T, uint4>::kN;  // of values: they are not turned
-    __shared__ int32_t tokens[kMaxPage];      // the page's new tokens, from the first one on,
-    __shared__ uint16_t offs[kMaxPage];       // and where in the page they go
-    __shared__ uint32_t is_new[kMaxPage / 32];
-    __shared__ int32_t n_tokens, last_pos;
-    __shared__ Piece red[kWarps][32][4];      // minima and maxima of a lane's two pieces
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
+    const int32_t seq = __ldg(a.token_seq + i), entry = __ldg(a.token_pos + i) >> m.page_shift;
+    Piece lo[2], hi[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) lo[x] = V::all(V::W::kInf), hi[x] = V::all(V::W::kNegInf);
+    auto see = [&](const Piece& x, const Piece& y) {
+        take<V, false>(lo[0], x), take<V, true>(hi[0], x);
+        take<V, false>(lo[1], y), take<V, true>(hi[1], y);
+    };
+    // The page's tokens go on to the first token of another page.
+    int32_t last = 0;
+    uint32_t is_new = 0;  // bit b of lane l: position 32 l + b
+    int32_t n_new = 0;
+    for (int64_t base = i;; base += 32) {
+        const int64_t t = base + lane;
+        const int32_t s = t < a.n_tokens ? __ldg(a.token_seq + t) : INT32_MAX;
+        const int32_t q = s >= 0 && s < INT32_MAX ? __ldg(a.token_pos + t) : -1;
+        bool in = s == seq && q >= 0 && q >> m.page_shift == entry;
+        const uint32_t stops = __ballot_sync(0xffffffffu, s >= 0 && !in);
+        in &= lane < (stops ? __ffs(stops) - 1 : 32);
+        const uint32_t tokens = __ballot_sync(0xffffffffu, in);
+        const int32_t off = q & (m.page - 1);
+        n_new += __popc(tokens);
+        if (tokens) {
+            const int32_t top = __reduce_max_sync(0xffffffffu, in ? off : 0);
+            last = max(last, top);
+            for (int32_t w = __reduce_min_sync(0xffffffffu, in ? off : INT32_MAX) >> 5; w <= top >> 5; ++w) {
+                const uint32_t bits = __reduce_or_sync(0xffffffffu, in && off >> 5 == w ? 1u << (off & 31) : 0);
+                if (lane == w) is_new |= bits;
+            }
+            const int32_t end = 32 - __clz(tokens);
+            constexpr int kAhead = 2;
+#pragma unroll 1
+            for (int32_t r = sub * kAhead * L.rows; r < end; r += split * kAhead * L.rows) {
+                Piece x[kAhead], y[kAhead];
+                int32_t pos[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int32_t at = r + u * L.rows + L.row;
+                    const bool mine = L.row < L.rows && at < end && (tokens >> at & 1);
+                    pos[u] = __shfl_sync(0xffffffffu, q, at & 31);
+                    if (!mine || (a.rope && pos[u] >= a.rope_len)) pos[u] = -1;
+                    const T* src = (const T*)a.k + (base + at) * a.k_stride + (int64_t)g * m.d;
+                    load_if(x[u], src + L.a, mine);
+                    load_if(y[u], src + L.b, mine && L.b >= 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (pos[u] < 0) continue;
+                    if (L.pair >= 0) {
+                        Angles<V> ang;
+                        ang.load(a.rope + (int64_t)pos[u] * a.rope_dim, a.rope_dim / 2, L.pair);
+                        ang.turn(x[u], y[u], a.interleaved);
+                    }
+                    see(x[u], y[u]);
+                }
+            }
+        }
+        if (stops) break;
+        if (!__any_sync(0xffffffffu, s >= 0)) {  // padding: on to what comes after it
+            const int64_t n = token_beside<true>(a, base + 31, lane);
+            if (n < 0) break;
+            base = n - 32;
+        }
+    }
+    if (n_new <= last) {  // keys that were there
+        const T* kc = (const T*)a.k_cache + paged_row(m, page, g, 0);
+        constexpr int kAhead = 4;
+#pragma unroll 1
+        for (int32_t off0 = sub * kAhead * L.rows; off0 < last; off0 += split * kAhead * L.rows) {
+            Piece x[kAhead], y[kAhead];
+            bool in[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int32_t off = off0 + u * L.rows + L.row;
+                const uint32_t bits = __shfl_sync(0xffffffffu, is_new, off >> 5 & 31);
+                in[u] = L.row < L.rows && off < last && !(bits >> (off & 31) & 1);
+                load_if(x[u], kc + off * m.token_stride + L.a, in[u]);
+                load_if(y[u], kc + off * m.token_stride + L.b, in[u] && L.b >= 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (in[u]) see(x[u], y[u]);
+        }
+    }
+    for (int r = 1; r < L.rows; ++r) {  // the lanes of the first row take the others'
+        const int from = (lane + r * L.per_row) & 31;
+        auto other = [&](const Piece& x) {
+            Piece y;
+#pragma unroll
+            for (int k = 0; k < V::kWords; ++k) word(y, k) = __shfl_sync(0xffffffffu, word(x, k), from);
+            return y;
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const Piece l = other(lo[x]), h = other(hi[x]);
+            if (lane < L.per_row) take<V, false>(lo[x], l), take<V, true>(hi[x], h);
+        }
+    }
+    if (split > 1) {
+        red[sub][lane][0] = lo[0], red[sub][lane][1] = lo[1], red[sub][lane][2] = hi[0], red[sub][lane][3] = hi[1];
+        __syncthreads();
+        for (int w = 1; w < split; ++w)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) take<V, false>(lo[x], red[w][lane][x]), take<V, true>(hi[x], red[w][lane][2 + x]);
+        __syncthreads();
+    }
+    if (sub == 0 && lane < L.per_row) {
+        T* dst = (T*)a.k_bounds + ((int64_t)page * m.hkv + g) * 2 * m.d;
+        *reinterpret_cast<Piece*>(dst + L.a) = lo[0];
+        *reinterpret_cast<Piece*>(dst + m.d + L.a) = hi[0];
+        if (L.b >= 0) {
+            *reinterpret_cast<Piece*>(dst + L.b) = lo[1];
+            *reinterpret_cast<Piece*>(dst + m.d + L.b) = hi[1];
+        }
+    }
+}
+
+// Blocks [0, check_blocks): what is wrong with the tokens, and the bounds of the pages whose first token of the call is
+// among a unit's `slice`, at one kv head; a unit has `split` warps. The other blocks: rows.
+template <typename V>
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(PagedMeta m, AppendArgs a, int32_t* status, int64_t check_blocks,
+                                                             int32_t slice, int32_t split) {
+    __shared__ typename V::Piece red[kWarps][32][4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     after_previous();
     if (__syncthreads_or(status_bad(status))) return;
-
-    if (blockIdx.x >= kv_blocks) {
-        const int32_t per_token = (m.hq + heads - 1) / heads;
-        const int64_t unit = (blockIdx.x - kv_blocks) * kWarps + warp, i = unit / per_token;
-        const int32_t h0 = (int32_t)(unit - i * per_token) * heads;
-        if (i < a.n_tokens) append_queries<V, 4>(m, a, i, h0, min(h0 + heads, m.hq), lane);
+    if (blockIdx.x >= check_blocks) {
+        append_rows<V>(m, a, (blockIdx.x - check_blocks) * kWarps + warp, lane, status);
         return;
     }
-
-    const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
-    const int v_row = m.d / kN, v_rows = 32 / v_row;  // values: a lane per piece
-    // Which of the slice's tokens are the first of a page: a lane per token, the same in every warp.
-    const int64_t i0 = blockIdx.x * (int64_t)slice;
-    uint32_t firsts = page_firsts(m, a, i0, slice, lane, warp == 0, status);
+    const int32_t heads = a.k_bounds ? m.hkv : 1, sub = warp % split;
+    const int64_t unit = ((int64_t)blockIdx.x * kWarps + warp) / split, i0 = unit / heads * slice;
+    const int32_t g = (int32_t)(unit % heads);
+    uint32_t firsts = page_firsts(m, a, i0, slice, lane, g == 0 && sub == 0, status);
+    if (!a.k_bounds) return;
     for (; firsts; firsts &= firsts - 1) {
-        // Every thread of the block takes the same way.
         const int64_t i = i0 + __ffs(firsts) - 1;
-        const int32_t seq = __ldg(a.token_seq + i), entry = __ldg(a.token_pos + i) >> m.page_shift;
-        const int32_t page = paged_page(m, a.table + seq * m.table_stride, entry, status);
-        if (page < 0) continue;
-
-        // The page's tokens: from here to the first token of another page.
-        __syncthreads();  // the previous page is done with shared memory
-        if (tid == 0) n_tokens = 0, last_pos = 0;
-        for (int x = tid; x < (m.page + 31) / 32; x += kThreads) is_new[x] = 0;
-        __syncthreads();
-        for (int64_t base = i;; base += kThreads) {
-            const int64_t t = base + tid;
-            const int32_t s = t < a.n_tokens ? __ldg(a.token_seq + t) : INT32_MAX;
-            const int32_t q = s >= 0 && s < INT32_MAX ? __ldg(a.token_pos + t) : -1;
-            const bool in = s == seq && q >= 0 && q >> m.page_shift == entry && !(a.rope && q >= a.rope_len);
-            const uint32_t stops = __ballot_sync(0xffffffffu, s >= 0 && !in);
-            // The first thread that sees another page's token ends the run; later tokens of this page (out of order) are
-            // somebody else's.
-            __shared__ int32_t stop;
-            if (tid == 0) stop = kThreads;
-            __syncthreads();
-            if (lane == 0 && stops) atomicMin(&stop, warp * 32 + __ffs(stops) - 1);
-            __syncthreads();
-            const int32_t end = stop;
-            if (in && tid < end) {
-                const int32_t k = atomicAdd(&n_tokens, 1), off = q & (m.page - 1);
-                if (k < kMaxPage) tokens[k] = (int32_t)(t - i), offs[k] = (uint16_t)off;
-                atomicOr(&is_new[off >> 5], 1u << (off & 31));
-                atomicMax(&last_pos, off);
-            }
-            __syncthreads();
-            if (end < kThreads) break;
-        }
-        const int32_t n = min(n_tokens, kMaxPage), last = last_pos;
-
-        // Tasks: kv head, and where there are fewer heads than warps a share of the rows.
-        const int32_t subs = max(1, kWarps / m.hkv);
-        for (int32_t task0 = 0; task0 < m.hkv * subs; task0 += kWarps) {
-            const int32_t task = task0 + warp, g = task / subs, sub = task - g * subs;
-            const bool work = task < m.hkv * subs;
-            Piece lo[2], hi[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                lo[x] = V::all(V::W::kInf);
-                hi[x] = V::all(V::W::kNegInf);
-            }
-            T* kc = (T*)a.k_cache + paged_row(m, page, work ? g : 0, 0);
-            T* vc = (T*)a.v_cache + paged_row(m, page, work ? g : 0, 0);
-            // Loads of several rows at a time, then what is done with them.
-            if (work && L.row < L.rows && a.k_bounds) {  // keys that were there
-                constexpr int kAhead = 4;
-                for (int32_t off = sub * L.rows + L.row; off < last; off += kAhead * subs * L.rows) {
-                    Piece x[kAhead], y[kAhead];
-                    bool in[kAhead];
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u) {
-                        const int32_t at = off + u * subs * L.rows;
-                        in[u] = at < last && !(is_new[at >> 5] >> (at & 31) & 1);
-                        const T* src = kc + at * m.token_stride;
-                        load_if(x[u], src + L.a, in[u]);
-                        load_if(y[u], src + L.b, in[u] && L.b >= 0);
-                    }
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u) {
-                        if (!in[u]) continue;
-                        take<V, false>(lo[0], x[u]), take<V, true>(hi[0], x[u]);
-                        take<V, false>(lo[1], y[u]), take<V, true>(hi[1], y[u]);  // (not used where there is no second piece)
-                    }
-                }
-            }
-            // New keys and values together: as many loads in flight as the two have.
-            constexpr int kKeys = 2, kValues = 4;
-            const int c = lane % v_row * kN, steps = kKeys * subs * L.rows, v_steps = kValues * subs * v_rows;
-            int32_t k0 = work && L.row < L.rows ? sub * L.rows + L.row : n;
-            int32_t v0 = work && lane < v_rows * v_row ? sub * v_rows + lane / v_row : n;
-            for (; k0 < n || v0 < n; k0 += steps, v0 += v_steps) {
-                Piece x[kKeys], y[kKeys];
-                uint4 z[kValues];
-                Angles<V> ang[kKeys];
-                int32_t off[kKeys];
-#pragma unroll
-                for (int u = 0; u < kKeys; ++u) {
-                    const int32_t at = k0 + u * subs * L.rows;
-                    const bool in = at < n;
-                    off[u] = in ? offs[at] : -1;
-                    const T* src = (const T*)a.k + (i + (in ? tokens[at] : 0)) * a.k_stride + g * m.d;
-                    load_if(x[u], src + L.a, in);
-                    load_if(y[u], src + L.b, in && L.b >= 0);
-                }
-#pragma unroll
-                for (int u = 0; u < kValues; ++u) {
-                    const int32_t at = v0 + u * subs * v_rows;
-                    z[u] = ldg_stream_if((const T*)a.v + (i + (at < n ? tokens[at] : 0)) * a.v_stride + g * m.d + c, at < n);
-                }
-#pragma unroll
-                for (int u = 0; u < kKeys; ++u)
-                    if (off[u] >= 0 && L.pair >= 0)
-                        ang[u].load(a.rope + ((int64_t)entry * m.page + off[u]) * a.rope_dim, a.rope_dim / 2, L.pair);
-#pragma unroll
-                for (int u = 0; u < kKeys; ++u) {
-                    if (off[u] < 0) continue;
-                    if (L.pair >= 0) ang[u].turn(x[u], y[u], a.interleaved);
-                    T* dst = kc + off[u] * m.token_stride;
-                    *reinterpret_cast<Piece*>(dst + L.a) = x[u];
-                    if (L.b >= 0) *reinterpret_cast<Piece*>(dst + L.b) = y[u];
-                    take<V, false>(lo[0], x[u]), take<V, true>(hi[0], x[u]);
-                    take<V, false>(lo[1], y[u]), take<V, true>(hi[1], y[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < kValues; ++u) {
-                    const int32_t at = v0 + u * subs * v_rows;
-                    if (at < n) *reinterpret_cast<uint4*>(vc + offs[at] * m.token_stride + c) = z[u];
-                }
-            }
-            if (!a.k_bounds) continue;
-            red[warp][lane][0] = lo[0], red[warp][lane][1] = lo[1], red[warp][lane][2] = hi[0], red[warp][lane][3] = hi[1];
-            __syncthreads();
-            // The first warp of a head joins the head's lanes: a thread per (minimum or maximum, piece of a row).
-            if (work && sub == 0) {
-                const int32_t warps = min(subs, m.hkv * subs - task);
-                for (int x = lane; x < 2 * L.per_row; x += 32) {
-                    const bool top = x >= L.per_row;
-                    const int j = top ? x - L.per_row : x;
-                    const Lanes J = lanes_of<V>(m.d, a.rope_dim, a.interleaved, j);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int c = half ? J.b : J.a;
-                        if (c < 0) continue;
-                        Piece best = red[warp][j][half + (top ? 2 : 0)];
-                        for (int w = 0; w < warps; ++w)
-                            for (int r = 0; r < L.rows; ++r) {
-                                const Piece y = red[warp + w][r * L.per_row + j][half + (top ? 2 : 0)];
-                                if (top) take<V, true>(best, y); else take<V, false>(best, y);
-                            }
-                        *reinterpret_cast<Piece*>((T*)a.k_bounds + (((int64_t)page * m.hkv + g) * 2 + top) * m.d + c) = best;
-                    }
-                }
-            }
-            __syncthreads();
-        }
+        const int32_t* row = a.table + __ldg(a.token_seq + i) * m.table_stride;
+        const int32_t page = paged_page(m, row, __ldg(a.token_pos + i) >> m.page_shift, status);
+        if (page >= 0) page_bounds<V>(m, a, i, page, g, split, sub, lane, red);
     }
 }
 
@@ -722,32 +645,28 @@ template <typename V>
 cudaError_t launch_pieces(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
     using T = typename V::T;
     constexpr int kSms = 148;
-    // A block per token while there are few; then as many tokens a block as leave several blocks per SM.
-    const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens / (kSms * 4)));
-    const int64_t kv_blocks = (a.n_tokens + slice - 1) / slice;
     const int rows = 32 / (a.rope_dim / 2 / V::kN + ((m.d - a.rope_dim) / V::kN + 1) / 2);
-    const int64_t all = a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv);
-    // From about what the SMs hold at once the rows stream. 32/4 heads, d 128, 500 tokens (5000 warps' rows): pages of 64
-    // 8.9 us so and 13.5 page by page, pages of 16 11.4 and 9.6; 2000 tokens 14.0 and 19.1, 16.4 and 20.3; 8000 tokens 37
-    // and 66, 37 and 71.
-    if (all / rows >= kSms * 32) {
-        const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
-        // Tokens a warp looks through for pages: few where each may be a page of its own (1000 sequences' tokens, 32/8 heads:
-        // 32 a warp 70 us, so 18), many where there are enough warps.
-        const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens * m.hkv / (kSms * 16)));
-        const int64_t slices = (a.n_tokens + slice - 1) / slice * (a.k_bounds ? m.hkv : 1);
-        cudaError_t e = launch_overlapped(append_stream_kernel<V>, (units + kStreamWarps - 1) / kStreamWarps,
-                                          kStreamThreads, 0, st, m, a, status);
-        if (e == cudaSuccess)
-            e = launch_overlapped(a.k_bounds ? append_bounds_stream_kernel<T> : append_order_kernel,
-                                  (slices + kStreamWarps - 1) / kStreamWarps, kStreamThreads, 0, st, m, a, status, slice);
-        return note_error(e, "paged append");
+    const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
+    const int64_t row_blocks = (units + kWarps - 1) / kWarps;
+    // Tokens that are looked through for pages at a time: few where each may be a page of its own (1000 sequences' tokens,
+    // 32/8 heads: 32 at a time 70 us, so 18), many where there are enough warps.
+    const int32_t heads = a.k_bounds ? m.hkv : 1;
+    const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens * heads / (kSms * 16)));
+    const int64_t slices = (a.n_tokens + slice - 1) / slice * heads;
+    // One launch or two. 32/4 heads, d 128, bf16: 1 token 4.8 us and 5.1, 251 tokens, 32/8 heads (3012 warps' rows) 10.9 and
+    // 11.6; 400 tokens of a sequence in pages of 64 (4000) 12.6 and 8.4, 16000 tokens 92 and 74.
+    if (a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv) / rows < kSms * 24) {
+        // A page is shared by a block's warps where it is long (one token, pages of 128: 4.9 us, by one warp 6.0; of 1024: 12.5, 35.5).
+        const int32_t split = a.k_bounds && m.page > 16 && slices <= kSms * 8 ? kWarps : 1;
+        const int64_t check_blocks = (slices * split + kWarps - 1) / kWarps;
+        return note_error(launch_overlapped(append_kernel<V>, check_blocks + row_blocks, kThreads, 0, st, m, a, status,
+                                            check_blocks, slice, split),
+                          "paged append");
     }
-    const int32_t heads = std::min(m.hq, rows);
-    const int64_t q_blocks = a.q ? (a.n_tokens * ((m.hq + heads - 1) / heads) + kWarps - 1) / kWarps : 0;
-    return note_error(launch_overlapped(append_kernel<V>, kv_blocks + q_blocks, kThreads, 0, st, m, a, status,
-                                        kv_blocks, slice, heads),
-                      "paged append");
+    cudaError_t e = launch_overlapped(append_rows_kernel<V>, row_blocks, kThreads, 0, st, m, a, status);
+    if (e == cudaSuccess)
+        e = launch_overlapped(append_bounds_kernel<T>, (slices + kWarps - 1) / kWarps, kThreads, 0, st, m, a, status, slice);
+    return note_error(e, "paged append");
 }
 
 // 16 bytes a piece where half of rope_dim is a multiple of them, 8 where it is of those (16000 tokens, 32/4 heads, d 80,
@@ -757,8 +676,8 @@ cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cud
     const int half = a.rope_dim / 2;
     if (half % Vec<T, uint4>::kN == 0) return launch_pieces<Vec<T, uint4>>(m, a, status, st);
     if (half % Vec<T, uint2>::kN == 0) return launch_pieces<Vec<T, uint2>>(m, a, status, st);
-    append_rows_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
-    if (a.k_bounds) append_bounds_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+    append_channels_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
+    if (a.k_bounds) append_channels_bounds_kernel<T><<<(unsigned)a.n_tokens, 128, 0, st>>>(m, a, status);
     return note_error(cudaGetLastError(), "paged append");
 }
 

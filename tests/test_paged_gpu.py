@@ -461,6 +461,42 @@ def test_append_many_tokens_bad_ones_raise_the_status(what, bit):
     assert kv.status_value() == bit
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page", [1, 8, 64, 1024])
+@pytest.mark.parametrize("length,step", [(100, 3), (100, 33), (2000, 700), (9000, 2), (30000, 7)])
+def test_append_between_cached_positions(dtype, page, length, step):
+    # Every step-th position is written anew, with padding here and there: the others keep their keys, and the bounds of a
+    # page are those of both up to its last new key.
+    hq, hkv, d = 8, 2, 64
+    c = Case([length, 50], hq, hkv, d, page, dtype)
+    kb = torch.zeros(c.k.shape[0], hkv, 2, d, dtype=dtype, device="cuda")
+    kv = PagedKV(hq, hkv, d, page, max_seqs=2, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    pos = torch.arange(1, length, step, dtype=torch.int32)
+    seq = torch.zeros_like(pos)
+    gap = torch.full((40,), -1, dtype=torch.int32)
+    at = len(pos) // 2
+    pos, seq = torch.cat((pos[:at], gap, pos[at:])).cuda(), torch.cat((seq[:at], gap, seq[at:])).cuda()
+    new = torch.randn(len(pos), 2, hkv, d, device="cuda").to(dtype)
+    before_k, before_v = c.k.clone(), c.v.clone()
+    kv.append(new[:, 0], new[:, 1], c.table, seq, pos)
+    kv.check_status()
+    real = seq >= 0
+    p = pos[real].long()
+    where = c.table[0, p // page].long()
+    before_k[where, :, p % page] = new[real, 0]
+    before_v[where, :, p % page] = new[real, 1]
+    assert torch.equal(c.k.nan_to_num(77.0), before_k.nan_to_num(77.0))
+    assert torch.equal(c.v.nan_to_num(77.0), before_v.nan_to_num(77.0))
+    want = torch.zeros_like(kb)
+    last = {}
+    for e, off in zip((p // page).tolist(), (p % page).tolist()):
+        last[e] = off
+    for e, off in last.items():
+        keys = before_k[c.table[0, e].long(), :, : off + 1]
+        want[c.table[0, e].long(), :, 0], want[c.table[0, e].long(), :, 1] = keys.amin(1), keys.amax(1)
+    assert torch.equal(kb, want)
+
+
 def test_append_follows_a_sequence_that_was_cut_back():
     # Ten positions written, five of them given up, one written anew: the bounds are those of the six that count.
     c = run_append([10], [10], 4, 2, 64, 16, BF, 64, False)
