@@ -135,12 +135,13 @@ class PagedKV:
             return fn(*args)
 
     def _table(self, page_table, what):
-        if (page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.get_device() != self._dev or
-                (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        shape, strides = page_table.shape, page_table.stride()
+        if (page_table.dtype is not _I32 or len(shape) != 2 or page_table.get_device() != self._dev or
+                (shape[1] > 1 and strides[1] != 1)):
             raise SplitKVError(EINVAL, f"{what}: page_table must be an int32 [n_seqs, pages] tensor on the cache's "
                                "device, its rows dense")
-        n, width = page_table.shape
-        stride = page_table.stride(0) if n > 1 else width
+        n, width = shape
+        stride = strides[0] if n > 1 else width
         if n > self.max_seqs or not 1 <= width <= self.max_pages or stride < width:
             raise SplitKVError(EINVAL, f"{what}: a page table of {n} x {width}, {stride} apart; made for up to "
                                f"{self.max_seqs} x {self.max_pages}, apart")
