@@ -17,8 +17,7 @@ namespace {
 // 128 threads a block 140 us, 256 143, 512 149 (35k tokens, 32/4 heads).
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 
-// Where token i goes. Padding and tokens out of range have page -1; the order is checked against the token
-// before it that is not padding.
+// Where token i goes. Padding and tokens out of range have page -1.
 __device__ TokenPlace token_place(const PagedMeta& m, const AppendArgs& a, int64_t i, int32_t* status) {
     TokenPlace t{__ldg(a.token_seq + i), __ldg(a.token_pos + i), -1};
     if (t.seq < 0) return t;
@@ -407,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 8) append_rows_kernel(PagedMeta m, A
 // head, the bounds of the pages whose first token of the call is among a warp's `slice`, from L2.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 7) append_bounds_kernel(PagedMeta m, AppendArgs a, int32_t* status,
-                                                                                int32_t slice) {
+                                                                   int32_t slice) {
     using V = Vec<T, uint4>;
     const int lane = threadIdx.x & 31;
     const int32_t heads = a.k_bounds ? m.hkv : 1;

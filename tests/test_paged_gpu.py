@@ -11,6 +11,8 @@ sums of n terms by n 2^-23 more. So
     |lse - ref| <= e' + n 2^-23 + 2^-23 |ref|.
 Rotations: two products and a sum in float32 (3 roundings of 2^-24 on |x| + |y|), then one rounding to the type.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -700,6 +702,37 @@ def test_graphs_follow_their_inputs_and_share_nothing():
     c.check(*outs[1], refs[1])
     c.check(*eager, refs[0])
     c.kv.check_status()
+
+
+def test_threads_share_one_object():
+    # Each thread on a stream of its own: decode, select and decode over the list, all on one object.
+    c = Case([9000, 50, 0, 700], 8, 2, 64, 16)
+    kb = torch.randn(c.k.shape[0], 2, 2, 64, device="cuda").sort(2).values.to(BF)
+    kv = PagedKV(8, 2, 64, 16, max_seqs=4, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    o, lse = kv.decode(c.q, c.table, c.lens)
+    pages = kv.select(c.q, c.table, c.lens, 20)
+    so, slse = kv.decode(c.q, c.table, c.lens, pages=pages)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(40):
+                a = kv.decode(c.q, c.table, c.lens)
+                p = kv.select(c.q, c.table, c.lens, 20)
+                b = kv.decode(c.q, c.table, c.lens, pages=p)
+                if not all(torch.equal(x, y) for x, y in zip((*a, p, *b), (o, lse, pages, so, slse))):
+                    wrong.append(1)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    kv.check_status()
 
 
 def test_an_eager_call_beside_a_capture_stays_out_of_it():
