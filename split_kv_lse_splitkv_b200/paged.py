@@ -57,7 +57,8 @@ class PagedKV:
     tables and token lists are read on the device, so a call captured into a CUDA graph follows their values at each
     replay. The object's scratch is shared by its decode calls: on a change of stream the new one waits for the old
     one, and a captured call has scratch of its own. A stream given by its handle has to outlive the object. Results
-    carry no autograd history. Errors that only the device sees collect in :attr:`status`.
+    carry no autograd history. Errors that only the device sees collect in :attr:`status`; while it is not zero, calls
+    do no work (:meth:`check_status` raises; zero it to go on).
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, max_seqs, max_pages, n_pages=None, dtype=None,
