@@ -27,7 +27,9 @@ constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kLoads = 8;         // copies of 16 bytes of bounds a lane makes in a round
 constexpr int kStages = 3;        // rounds in flight and in use
 constexpr int kRing = kWarps * kStages * kLoads * 32;  // 16-byte pieces: 192 KB
-constexpr int kInShared = 16384;  // scores that the second kernel keeps in shared memory; longer rows stay in L2
+// Scores that the second kernel keeps in shared memory, 192 KB; longer rows stay in L2. 8 rows of 18750 pages: 36 us so, from L2
+// 50; 16 rows of 43750: 111, 145.
+constexpr int kInShared = 49152;
 constexpr int kCands = 512;       // pages that are ranked one by one
 constexpr int kWords = 512, kSpan = kWords * 32;
 static_assert(kWords == kThreads && kCands <= kThreads, "one word, one candidate a thread");
