@@ -27,9 +27,10 @@ constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kLoads = 8;         // copies of 16 bytes of bounds a lane makes in a round
 constexpr int kStages = 3;        // rounds in flight and in use
 constexpr int kRing = kWarps * kStages * kLoads * 32;  // 16-byte pieces: 192 KB
-// Scores that the second kernel keeps in shared memory, 192 KB; longer rows stay in L2. 8 rows of 18750 pages: 36 us so, from L2
-// 50; 16 rows of 43750: 111, 145.
-constexpr int kInShared = 49152;
+// Scores that the second kernel keeps in shared memory (192 KB, or 92 where two blocks share an SM); longer rows stay in L2. 8
+// rows of 18750 pages: 36 us so, from L2 50; 16 rows of 43750: 111, 145.
+template <int kPerSm>
+constexpr int kInShared = kPerSm == 1 ? 49152 : 23552;
 constexpr int kCands = 512;       // pages that are ranked one by one
 constexpr int kWords = 512, kSpan = kWords * 32;
 static_assert(kWords == kThreads && kCands <= kThreads, "one word, one candidate a thread");
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pick_kernel(PagedMeta m, con
         return;
     }
     Keys<uint32_t> keys{copy, r.count, 1};
-    if (r.count > kInShared) keys = {reinterpret_cast<uint32_t*>(scores), r.count, 2};
+    if (r.count > kInShared<kPerSm>) keys = {reinterpret_cast<uint32_t*>(scores), r.count, 2};
     uint32_t lo = ~0u, hi = 0;
     float size = 0.f;
     auto see = [&](int32_t p, const uint2& x) {
@@ -642,7 +643,8 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     const bool many = (int64_t)m.n_seqs * m.hkv > sms;
     auto pick = many ? pick_kernel<T, 2> : pick_kernel<T, 1>;
     static SmemGrants granted[2];
-    e = allow_smem((const void*)pick, sizeof(uint32_t) * kInShared, granted[many]);
+    const int in_shared = many ? kInShared<2> : kInShared<1>;
+    e = allow_smem((const void*)pick, sizeof(uint32_t) * in_shared, granted[many]);
     if (e != cudaSuccess) return e;
     auto score = score_kernel<T, LP, NC>;
     static SmemGrants score_granted;
@@ -652,7 +654,7 @@ cudaError_t launch(const PagedMeta& m, const void* q, int64_t q_stride, const vo
     e = launch_overlapped(score, sms, kThreads, lens, st, m, (const T*)q, q_stride, (const T*)k_bounds,
                           table, seq_len, n_select, keep_first, keep_last, (uint2*)ws, status);
     if (e == cudaSuccess)
-        e = launch_overlapped(pick, m.n_seqs * m.hkv, kThreads, sizeof(uint32_t) * std::min(m.max_pages, kInShared), st, m,
+        e = launch_overlapped(pick, m.n_seqs * m.hkv, kThreads, sizeof(uint32_t) * std::min(m.max_pages, in_shared), st, m,
                               (const T*)q, q_stride, (const T*)k_bounds, table, seq_len, n_select, keep_first,
                               keep_last, (uint2*)ws, pages, status);
     return note_error(e, "paged select");

@@ -576,7 +576,7 @@ def test_select_ties_and_long_rows(count, n_select):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("n_seqs,count,n_select", [(100, 6000, 50), (1, 131072, 1000), (90, 700, 699), (2, 49152, 900),
-                                                   (80, 20000, 30), (1, 49153, 64)])
+                                                   (80, 24000, 30), (1, 49153, 64)])
 def test_select_many_rows_and_the_longest(dtype, n_seqs, count, n_select):
     g = torch.Generator().manual_seed(count)
     d, hkv, hq = 16, 2, 6
