@@ -66,9 +66,10 @@ __device__ T rotated(const AppendArgs& a, const T* x, int32_t i, const float* cs
 }
 
 // ---- any rope_dim: channels one by one. One block per token: queries, keys and values.
+// Both kernels leave as whole blocks: other blocks raise the status word meanwhile, and token_beside() needs all lanes.
 template <typename T>
 __global__ void __launch_bounds__(128) append_channels_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
-    if (status_bad(status)) return;
+    if (__syncthreads_or(status_bad(status))) return;
     const int64_t i = blockIdx.x;
     const TokenPlace t = token_place(m, a, i, status);
     if (t.seq >= 0 && threadIdx.x < 32) {
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(128) append_channels_kernel(PagedMeta m, Appen
 // One block per token: the bounds of its page, if no later token of the call writes the same page.
 template <typename T>
 __global__ void __launch_bounds__(128) append_channels_bounds_kernel(PagedMeta m, AppendArgs a, int32_t* status) {
-    if (status_bad(status)) return;
+    if (__syncthreads_or(status_bad(status))) return;
     const int64_t i = blockIdx.x;
     const TokenPlace t = token_place(m, a, i, status);
     if (t.page < 0) return;

@@ -463,6 +463,28 @@ def test_append_many_tokens_bad_ones_raise_the_status(what, bit):
     assert kv.status_value() == bit
 
 
+@pytest.mark.parametrize("what,bit", [("order", B.DEV_TOKEN_ORDER), ("seq", B.DEV_BAD_TOKEN), ("page", B.DEV_BAD_PAGE)])
+def test_append_channels_bad_ones_raise_the_status_beside_others(what, bit):
+    # Channel by channel: blocks start and leave while others raise the status word, looking for tokens across padding.
+    n = 20000
+    c = Case([n], 4, 2, 64, 16)
+    kb = torch.zeros(c.k.shape[0], 2, 2, 64, dtype=BF, device="cuda")
+    kv = PagedKV(4, 2, 64, 16, max_seqs=1, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    seq[1::3] = -1
+    table = c.table.clone()
+    if what == "order":
+        pos[9000::3000] = 2
+    elif what == "seq":
+        seq[9000::3000] = 1
+    else:
+        table[0, 700::300] = c.k.shape[0]
+    x = torch.zeros(n, 2, 64, dtype=BF, device="cuda")
+    kv.append(x, x, table, seq, pos, q=torch.zeros(n, 4, 64, dtype=BF, device="cuda"), rope=rope_table(n, 10))
+    assert kv.status_value() & bit
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("page", [1, 8, 64, 1024])
 @pytest.mark.parametrize("length,step", [(100, 3), (100, 33), (2000, 700), (9000, 2), (30000, 7)])
