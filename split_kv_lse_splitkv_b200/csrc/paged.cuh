@@ -63,6 +63,9 @@ cudaError_t allow_smem(const void* kernel, size_t most, SmemGrants& granted);
 // calls after_previous(), which waits until that one has completed and its writes are seen, before it touches memory; or,
 // in the second kernel of a call, before it touches what the first one writes (the call's inputs are there once the first
 // one has let its dependents start). Hides the launch's own latency (2 us of every call), felt where a call takes ten.
+// So what these kernels read may be written while they are resident: they read it with coherent loads behind the wait, not
+// through the read-only path (ld.global.nc, __ldg, const __restrict__ parameters), which asks for data that does not change
+// while the kernel lives and which the compiler may move ahead of the wait.
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};
@@ -84,7 +87,7 @@ __device__ __forceinline__ void after_previous() {
 
 // Length of sequence b, or 0 (with the status bit) when it is not in [0, max_pages * page].
 __device__ __forceinline__ int32_t paged_len(const PagedMeta& m, const int32_t* seq_len, int32_t b, int32_t* status) {
-    const int32_t n = __ldg(seq_len + b);
+    const int32_t n = seq_len[b];
     if (n < 0 || n > (int64_t)m.max_pages * m.page) {
         raise_status(status, SPLITKV_DEV_BAD_LENGTH);
         return 0;
@@ -94,7 +97,7 @@ __device__ __forceinline__ int32_t paged_len(const PagedMeta& m, const int32_t* 
 
 // Cache page behind entry `e` of a page-table row, or -1 (with the status bit) when it is out of range.
 __device__ __forceinline__ int32_t paged_page(const PagedMeta& m, const int32_t* row, int32_t e, int32_t* status) {
-    const int32_t p = __ldg(row + e);
+    const int32_t p = row[e];
     if (p < 0 || p >= m.n_pages) {
         raise_status(status, SPLITKV_DEV_BAD_PAGE);
         return -1;
@@ -115,7 +118,7 @@ __device__ __forceinline__ uint4 ldg_stream_if(const void* p, bool in) {
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %5, 0;\n\t"
         "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        "@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
         : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
         : "l"(p), "r"((int)in));
     return r;

@@ -19,7 +19,7 @@ constexpr int kThreads = 128, kWarps = kThreads / 32;
 
 // Where token i goes. Padding and tokens out of range have page -1.
 __device__ TokenPlace token_place(const PagedMeta& m, const AppendArgs& a, int64_t i, int32_t* status) {
-    TokenPlace t{__ldg(a.token_seq + i), __ldg(a.token_pos + i), -1};
+    TokenPlace t{a.token_seq[i], a.token_pos[i], -1};
     if (t.seq < 0) return t;
     if (t.seq >= m.n_seqs || t.pos < 0 || t.pos >= (int64_t)m.max_pages * m.page ||
         (a.rope && t.pos >= a.rope_len)) {
@@ -41,7 +41,7 @@ __device__ __noinline__ int64_t token_beside(const AppendArgs& a, int64_t i, int
 #pragma unroll
         for (int u = 0; u < kLook; ++u) {
             const int64_t p = kAfter ? i + base + u * 32 + lane : i - base - u * 32 - lane;
-            real[u] = p >= 0 && p < a.n_tokens && __ldg(a.token_seq + p) >= 0;
+            real[u] = p >= 0 && p < a.n_tokens && a.token_seq[p] >= 0;
         }
 #pragma unroll
         for (int u = 0; u < kLook; ++u) {
@@ -125,7 +125,7 @@ __device__ __forceinline__ void load_if(uint2& x, const void* p, bool in) {
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %3, 0;\n\t"
         "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
+        "@p ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
         : "=&r"(x.x), "=&r"(x.y)
         : "l"(p), "r"((int)in));
 }
@@ -234,13 +234,13 @@ struct Angles {
 #pragma unroll
         for (int i = 0; i < V::kN; i += 4) {
             if constexpr (V::kN >= 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(row + pair + i));
-                const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + pair + i));
+                const float4 x = *reinterpret_cast<const float4*>(row + pair + i);
+                const float4 y = *reinterpret_cast<const float4*>(row + half + pair + i);
                 c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
                 s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
             } else {
-                const float2 x = __ldg(reinterpret_cast<const float2*>(row + pair));
-                const float2 y = __ldg(reinterpret_cast<const float2*>(row + half + pair));
+                const float2 x = *reinterpret_cast<const float2*>(row + pair);
+                const float2 y = *reinterpret_cast<const float2*>(row + half + pair);
                 c[0] = x.x, c[1] = x.y, s[0] = y.x, s[1] = y.y;
             }
         }
@@ -278,13 +278,13 @@ __device__ __forceinline__ uint32_t page_firsts(const PagedMeta& m, const Append
     if (i0 >= a.n_tokens) return 0;
     const int64_t i = i0 + lane;
     const bool mine = lane < slice && i < a.n_tokens;
-    const int32_t seq = mine ? __ldg(a.token_seq + i) : -1, pos = mine ? __ldg(a.token_pos + i) : 0;
-    int32_t before = i0 > 0 ? __ldg(a.token_seq + i0 - 1) : -1, before_pos = i0 > 0 ? __ldg(a.token_pos + i0 - 1) : -1;
+    const int32_t seq = mine ? a.token_seq[i] : -1, pos = mine ? a.token_pos[i] : 0;
+    int32_t before = i0 > 0 ? a.token_seq[i0 - 1] : -1, before_pos = i0 > 0 ? a.token_pos[i0 - 1] : -1;
     const uint32_t real = __ballot_sync(0xffffffffu, seq >= 0), below = real & ((1u << lane) - 1);
     if (!real) return 0;
     if (i0 > 0 && before < 0) {  // padding before the slice
         const int64_t p = token_beside<false>(a, i0 - 1, lane);
-        if (p >= 0) before = __ldg(a.token_seq + p), before_pos = __ldg(a.token_pos + p);
+        if (p >= 0) before = a.token_seq[p], before_pos = a.token_pos[p];
     }
     const int from = below ? 31 - __clz(below) : 0;
     const int32_t s = __shfl_sync(0xffffffffu, seq, from), p = __shfl_sync(0xffffffffu, pos, from);
@@ -351,7 +351,7 @@ __device__ __forceinline__ void append_rows(const PagedMeta& m, const AppendArgs
                 if (!in[k]) continue;
                 if (i[k] != now) {
                     now = i[k];
-                    const int32_t seq = __ldg(a.token_seq + now), pos = __ldg(a.token_pos + now);
+                    const int32_t seq = a.token_seq[now], pos = a.token_pos[now];
                     // A token that is out of range is reported with its keys; its queries pass as they are.
                     turn = L.pair >= 0 && seq >= 0 && pos >= 0 && pos < a.rope_len;
                     if (turn) ang.load(a.rope + (int64_t)pos * a.rope_dim, a.rope_dim / 2, L.pair);
@@ -420,13 +420,13 @@ __global__ void __launch_bounds__(kThreads, 7) append_bounds_kernel(PagedMeta m,
     if (!firsts) after_previous();
     for (; firsts; firsts &= firsts - 1) {
         const int64_t i = i0 + __ffs(firsts) - 1;
-        const int32_t seq = __ldg(a.token_seq + i), entry = __ldg(a.token_pos + i) >> m.page_shift;
+        const int32_t seq = a.token_seq[i], entry = a.token_pos[i] >> m.page_shift;
         const int32_t page = paged_page(m, a.table + seq * m.table_stride, entry, status);
         int32_t last = 0;  // the last of the page's tokens: they go on to the first token of another page
         for (int64_t base = i;; base += 32) {
             const int64_t t = base + lane;
-            const int32_t s = t < a.n_tokens ? __ldg(a.token_seq + t) : INT32_MAX;
-            const int32_t q = s >= 0 && s < INT32_MAX ? __ldg(a.token_pos + t) : -1;
+            const int32_t s = t < a.n_tokens ? a.token_seq[t] : INT32_MAX;
+            const int32_t q = s >= 0 && s < INT32_MAX ? a.token_pos[t] : -1;
             const bool in = s == seq && q >= 0 && q >> m.page_shift == entry;
             const uint32_t stops = __ballot_sync(0xffffffffu, s >= 0 && !in);
             const int end = stops ? __ffs(stops) - 1 : 32;
@@ -498,7 +498,7 @@ __device__ __forceinline__ void page_bounds(const PagedMeta& m, const AppendArgs
     using T = typename V::T;
     using Piece = typename V::Piece;
     const Lanes L = lanes_of<V>(m.d, a.rope_dim, a.interleaved, lane);
-    const int32_t seq = __ldg(a.token_seq + i), entry = __ldg(a.token_pos + i) >> m.page_shift;
+    const int32_t seq = a.token_seq[i], entry = a.token_pos[i] >> m.page_shift;
     Piece lo[2], hi[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) lo[x] = V::all(V::W::kInf), hi[x] = V::all(V::W::kNegInf);
@@ -512,8 +512,8 @@ __device__ __forceinline__ void page_bounds(const PagedMeta& m, const AppendArgs
     int32_t n_new = 0;
     for (int64_t base = i;; base += 32) {
         const int64_t t = base + lane;
-        const int32_t s = t < a.n_tokens ? __ldg(a.token_seq + t) : INT32_MAX;
-        const int32_t q = s >= 0 && s < INT32_MAX ? __ldg(a.token_pos + t) : -1;
+        const int32_t s = t < a.n_tokens ? a.token_seq[t] : INT32_MAX;
+        const int32_t q = s >= 0 && s < INT32_MAX ? a.token_pos[t] : -1;
         bool in = s == seq && q >= 0 && q >> m.page_shift == entry;
         const uint32_t stops = __ballot_sync(0xffffffffu, s >= 0 && !in);
         in &= lane < (stops ? __ffs(stops) - 1 : 32);
@@ -635,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(PagedMeta m, Append
     if (!a.k_bounds) return;
     for (; firsts; firsts &= firsts - 1) {
         const int64_t i = i0 + __ffs(firsts) - 1;
-        const int32_t* row = a.table + __ldg(a.token_seq + i) * m.table_stride;
-        const int32_t page = paged_page(m, row, __ldg(a.token_pos + i) >> m.page_shift, status);
+        const int32_t* row = a.table + a.token_seq[i] * m.table_stride;
+        const int32_t page = paged_page(m, row, a.token_pos[i] >> m.page_shift, status);
         if (page >= 0) page_bounds<V>(m, a, i, page, g, split, sub, lane, red);
     }
 }

@@ -105,7 +105,7 @@ struct Frag<__nv_bfloat16, DP, NT> {
             for (int j = 0; j < DP / 32; ++j) {
                 const int c = 32 * j + 8 * t;
                 q[n][j] = n * 8 + g < rows && c < d
-                              ? __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(n * 8 + g) * d + c))
+                              ? *reinterpret_cast<const uint4*>(base + (int64_t)(n * 8 + g) * d + c)
                               : make_uint4(0, 0, 0, 0);
             }
     }
@@ -218,7 +218,7 @@ struct Frag<float, DP, NT> {
                 const int c = 16 * j + 4 * t;
                 q[(n * DP / 16 + j) * 32 + lane] =
                     n * 8 + g < rows && c < d
-                        ? __ldg(reinterpret_cast<const float4*>(base + (int64_t)(n * 8 + g) * d + c))
+                        ? *reinterpret_cast<const float4*>(base + (int64_t)(n * 8 + g) * d + c)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
             }
     }
@@ -405,13 +405,10 @@ struct Side {
 };
 
 template <typename T, int DP, int NT, int W>
-__global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
-                                                          const T* __restrict__ kc, const T* __restrict__ vc,
-                                                          const int32_t* __restrict__ table,
-                                                          const int32_t* __restrict__ seq_len,
-                                                          const int32_t* __restrict__ pages, int32_t n_select,
-                                                          T* __restrict__ o, float* __restrict__ lse, int32_t* status,
-                                                          uint32_t* counters, char* slots) {
+__global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T* q, int64_t q_stride, const T* kc,
+                                                          const T* vc, const int32_t* table, const int32_t* seq_len,
+                                                          const int32_t* pages, int32_t n_select, T* o, float* lse,
+                                                          int32_t* status, uint32_t* counters, char* slots) {
     static_assert(2 * W <= 32, "one lane per partial of the block");
     constexpr int R = 8 * NT, kCols = DP / 4, kThreads = W * 32;
     using P = Partial<DP, R>;
@@ -521,13 +518,13 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
         const int32_t g = sg.sub / row_groups, row0 = (sg.sub - g * row_groups) * R;
         const int32_t rows = min(R, m.group - row0);
         const int32_t* trow = table + sg.b * m.table_stride;
-        const int32_t len = __ldg(seq_len + sg.b), count = (len + m.page - 1) >> m.page_shift;
+        const int32_t len = seq_len[sg.b], count = (len + m.page - 1) >> m.page_shift;
         const int32_t* chosen = pages ? pages + ((int64_t)sg.b * m.hkv + g) * n_select : nullptr;
         const int32_t listed = chosen ? min(n_select, count) : 0;
         const int64_t head = (int64_t)g * m.head_stride;
         if (chosen && t_begin == 0 && row0 == 0)  // the unread tail of the list has to be empty
             for (int32_t i = listed + lane; i < n_select; i += 32)
-                if (__ldg(chosen + i) != -1) raise_status(status, SPLITKV_DEV_BAD_PAGE);
+                if (chosen[i] != -1) raise_status(status, SPLITKV_DEV_BAD_PAGE);
 
         // Page-table entry of the lane's row of tile i, or -1 (past the end, or not listed).
         auto entry_of = [&](int32_t i) -> int32_t {
@@ -535,14 +532,14 @@ __global__ void __launch_bounds__(W * 32, 1) decode_kernel(PagedMeta m, const T*
             if (i >= t_end) return -1;
             if (!chosen) return pos < len ? e : -1;
             if (e >= listed) return -1;
-            const int32_t x = __ldg(chosen + e);
+            const int32_t x = chosen[e];
             const bool first = (pos & (m.page - 1)) == 0 || (lane & 15) == 0;
             if (x < -1 || x >= count) {
                 raise_status(status, SPLITKV_DEV_BAD_PAGE);
                 return -1;
             }
             if (first && e > 0 && x >= 0) {
-                const int32_t y = __ldg(chosen + e - 1);
+                const int32_t y = chosen[e - 1];
                 if (y < 0 || y >= x) raise_status(status, SPLITKV_DEV_BAD_PAGE);
             }
             return x;

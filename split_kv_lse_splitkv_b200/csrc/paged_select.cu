@@ -97,11 +97,9 @@ __device__ __forceinline__ Row row_of(const PagedMeta& m, int32_t len, int32_t n
 // size times the largest size among the pages (2 instructions a pair of channels; a sum per page would take 4).
 // LP lanes hold the 2d channels of one page, NC chunks of 16 bytes each.
 template <typename T, int LP, int NC>
-__global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
-                                                         const T* __restrict__ bounds,
-                                                         const int32_t* __restrict__ table,
-                                                         const int32_t* __restrict__ seq_len, int32_t n_select,
-                                                         int32_t keep_first, int32_t keep_last, uint2* __restrict__ scores,
+__global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* q, int64_t q_stride, const T* bounds,
+                                                         const int32_t* table, const int32_t* seq_len, int32_t n_select,
+                                                         int32_t keep_first, int32_t keep_last, uint2* scores,
                                                          int32_t* status) {
     constexpr int kN = Chunk<T>::kN, kPer = 32 / LP;    // pages a warp reads with one load a lane
     constexpr int kV = kLoads / NC, kStep = kV * kPer;  // pages of a lane's round, of a warp's
@@ -404,12 +402,12 @@ __device__ __forceinline__ int32_t place(const Shared& sh, int32_t n) {
 }
 
 __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
     f[0] = __uint_as_float(x.x << 16), f[1] = __uint_as_float(x.x & 0xffff0000u);
     f[2] = __uint_as_float(x.y << 16), f[3] = __uint_as_float(x.y & 0xffff0000u);
 }
 __device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 x = *reinterpret_cast<const float4*>(p);
     f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
 }
 
@@ -534,11 +532,11 @@ __device__ __forceinline__ float error_of(const PagedMeta& m) { return (32 + 2 *
 // More rows than SMs want two there. 8 rows of 4096 pages, select as a whole: 13.7 us, 15.9 with two; 2048 rows of 250:
 // 118 us, 98 with two.
 template <typename T, int kPerSm>
-__global__ void __launch_bounds__(kThreads, kPerSm) pick_kernel(PagedMeta m, const T* __restrict__ q, int64_t q_stride,
-                                                        const T* __restrict__ bounds, const int32_t* __restrict__ table,
-                                                        const int32_t* __restrict__ seq_len, int32_t n_select,
-                                                        int32_t keep_first, int32_t keep_last, uint2* scores,
-                                                        int32_t* __restrict__ pages, int32_t* status) {
+__global__ void __launch_bounds__(kThreads, kPerSm) pick_kernel(PagedMeta m, const T* q, int64_t q_stride,
+                                                                const T* bounds, const int32_t* table,
+                                                                const int32_t* seq_len, int32_t n_select,
+                                                                int32_t keep_first, int32_t keep_last, uint2* scores,
+                                                                int32_t* pages, int32_t* status) {
     extern __shared__ uint32_t copy[];
     __shared__ __align__(16) Shared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

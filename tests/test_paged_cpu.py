@@ -1,5 +1,7 @@
 """The paged-cache operators without a GPU: the oracle against explicit formulas, and every refusal before a launch."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -307,3 +309,14 @@ def test_select_needs_bounds():
 def test_struct_matches_the_header():
     # The compiler's size of splitkv_paged: four int32, one int64, an int32 (padded), four int64, float, int32.
     assert ctypes.sizeof(B.Paged) == 16 + 8 + 8 + 32 + 8
+
+
+def test_kernels_launched_early_read_through_coherent_loads():
+    # They may be resident while the kernel before them writes what they read: the read-only path is not for that.
+    csrc = os.path.join(os.path.dirname(B.__file__), "csrc")
+    names = [n for n in os.listdir(csrc) if n.startswith("paged")]
+    assert len(names) == 4
+    for name in names:
+        with open(os.path.join(csrc, name)) as f:
+            code = "\n".join(line.split("//")[0] for line in f)
+        assert not re.search(r"__ldg|__restrict__|ld\.global\.nc|__constant__", code), name
