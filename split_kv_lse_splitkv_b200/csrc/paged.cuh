@@ -60,9 +60,9 @@ using SmemGrants = std::atomic<bool>[kMaxDevices];
 cudaError_t allow_smem(const void* kernel, size_t most, SmemGrants& granted);
 
 // Launch in which the kernel may be placed on the SMs while the one before it in the stream drains. Every thread of it
-// calls after_previous(), which waits until that one has completed and its writes are seen, before it touches memory; or,
-// in the second kernel of a call, before it touches what the first one writes (the call's inputs are there once the first
-// one has let its dependents start). Hides the launch's own latency (2 us of every call), felt where a call takes ten.
+// calls after_previous(), which waits until that one has completed and its writes are seen, before it touches memory. That
+// holds for the second kernel of a call too: that the first one has waited says nothing of what the second one sees. Hides
+// the launch's own latency (2 us of every call), felt where a call takes ten.
 // So what these kernels read may be written while they are resident: they read it with coherent loads behind the wait, not
 // through the read-only path (ld.global.nc, __ldg, const __restrict__ parameters), which asks for data that does not change
 // while the kernel lives and which the compiler may move ahead of the wait.

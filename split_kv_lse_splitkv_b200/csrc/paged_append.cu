@@ -414,10 +414,9 @@ __global__ void __launch_bounds__(kThreads, 7) append_bounds_kernel(PagedMeta m,
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), i0 = unit / heads * slice;
     const int32_t g = (int32_t)(unit % heads);
     const Lanes L = lanes_of<V>(m.d, 0, 0, lane);
+    after_previous();
     uint32_t firsts = page_firsts(m, a, i0, slice, lane, g == 0, status);
-    bool waited = false;
-    if (!a.k_bounds) firsts = 0;
-    if (!firsts) after_previous();
+    if (!a.k_bounds) return;
     for (; firsts; firsts &= firsts - 1) {
         const int64_t i = i0 + __ffs(firsts) - 1;
         const int32_t seq = a.token_seq[i], entry = a.token_pos[i] >> m.page_shift;
@@ -438,8 +437,6 @@ __global__ void __launch_bounds__(kThreads, 7) append_bounds_kernel(PagedMeta m,
                 base = n - 32;
             }
         }
-        if (!waited) after_previous();  // the keys
-        waited = true;
         if (page < 0 || __any_sync(0xffffffffu, status_bad(status))) continue;
         uint4 lo[2], hi[2];
 #pragma unroll

@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) pick_kernel(PagedMeta m, con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = blockIdx.x, b = row / m.hkv, g = row % m.hkv;
     scores += (int64_t)row * m.max_pages;
+    after_previous();
     const Row r = row_of(m, paged_len(m, seq_len, b, status), n_select, keep_first, keep_last);
-    after_previous();  // the scores
     constexpr int kAhead = kPerSm == 1 ? 8 : 4;  // scores of a thread that are loaded at once
     uint2 x[kAhead];
 #pragma unroll

@@ -697,6 +697,50 @@ def test_streams_share_one_object():
     assert torch.equal(raw[0], want[0])
 
 
+def test_calls_see_what_the_kernel_before_them_wrote():
+    # Lengths, tokens and queries change right before each call, without a wait: the results are those of calls made apart.
+    c = Case([4000, 3000, 9], 8, 2, 64, 16)
+    kb = torch.randn(c.k.shape[0], 2, 2, 64, device="cuda").sort(2).values.to(BF)
+    kv = PagedKV(8, 2, 64, 16, max_seqs=3, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    n = 6000  # two launches
+    inputs = []
+    for i in range(4):
+        g = torch.Generator().manual_seed(i)
+        inputs.append(dict(lens=torch.tensor([4000 - 700 * i, 100 + 900 * i, i], dtype=torch.int32),
+                           pos=torch.cat((torch.arange(3500) + 10 * i, torch.arange(2500) + 50 * i)).to(torch.int32),
+                           q=torch.randn(3, 8, 64, generator=g).to(BF), x=torch.randn(n, 2, 64, generator=g).to(BF)))
+    inputs = [{k: v.cuda() for k, v in x.items()} for x in inputs]
+    seq = torch.cat((torch.zeros(3500), torch.ones(2500))).to(torch.int32).cuda()
+    now = {k: v.clone() for k, v in inputs[0].items()}
+    state = [c.k, c.v, kb]
+    start = [t.clone() for t in state]
+
+    def step(x, apart):
+        got = []
+        for call in (lambda: kv.append(now["x"], now["x"], c.table, seq, now["pos"]),
+                     lambda: got.append(kv.select(now["q"], c.table, now["lens"], 30)),
+                     lambda: got.extend(kv.decode(now["q"], c.table, now["lens"])),
+                     lambda: got.extend(kv.decode(now["q"], c.table, now["lens"], pages=got[0]))):
+            for k, v in now.items():
+                v.copy_(x[k])
+            if apart:
+                torch.cuda.synchronize()
+            call()
+            if apart:
+                torch.cuda.synchronize()
+        return got + [t.clone() for t in state]
+
+    def run(apart):
+        for t, s in zip(state, start):
+            t.copy_(s)
+        return [step(inputs[i % 4], apart) for i in range(24)]
+
+    want, got = run(True), run(False)
+    kv.check_status()
+    for w, g in zip(want, got):
+        assert all(torch.equal(x.nan_to_num(77.0), y.nan_to_num(77.0)) for x, y in zip(w, g))
+
+
 def test_graphs_follow_their_inputs_and_share_nothing():
     # Two graphs of one object, replayed side by side with eager calls between: each keeps its results.
     c = Case([6000, 3000], 32, 4, 128, 16)
