@@ -702,7 +702,8 @@ def test_calls_see_what_the_kernel_before_them_wrote():
     c = Case([4000, 3000, 9], 8, 2, 64, 16)
     kb = torch.randn(c.k.shape[0], 2, 2, 64, device="cuda").sort(2).values.to(BF)
     kv = PagedKV(8, 2, 64, 16, max_seqs=3, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
-    n = 6000  # two launches
+    n = 6000  # with queries: two launches
+    many_q = torch.randn(n, 8, 64, device="cuda").to(BF)
     inputs = []
     for i in range(4):
         g = torch.Generator().manual_seed(i)
@@ -717,7 +718,7 @@ def test_calls_see_what_the_kernel_before_them_wrote():
 
     def step(x, apart):
         got = []
-        for call in (lambda: kv.append(now["x"], now["x"], c.table, seq, now["pos"]),
+        for call in (lambda: kv.append(now["x"], now["x"], c.table, seq, now["pos"], q=many_q),
                      lambda: got.append(kv.select(now["q"], c.table, now["lens"], 30)),
                      lambda: got.extend(kv.decode(now["q"], c.table, now["lens"])),
                      lambda: got.extend(kv.decode(now["q"], c.table, now["lens"], pages=got[0]))):
