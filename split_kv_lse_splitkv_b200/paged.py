@@ -99,6 +99,7 @@ class PagedKV:
         self._q_strides = (self.n_q_heads * self.head_dim, self.head_dim, 1)
         self._lock = threading.Lock()
         self._ws = self._stream = None
+        self._streams = set()  # those that _first_on has seen
         if self._index is None:
             self.status = torch.zeros(1, dtype=_I32, device=self.device)
         else:  # the status word and the scratch, whose counters start at zero: before any stream's first call
@@ -138,6 +139,17 @@ class PagedKV:
         _need(stream.device == self.device, "PagedKV: a stream of another device than the cache's")
         with torch.cuda.stream(stream):
             return fn(*args)
+
+    def _first_on(self, raw) -> None:
+        """The first call on the current stream. The object may be dropped while work of its calls is under way, on streams
+        other than those its tensors were allocated on: these are not to be given to anybody else before that is done."""
+        if torch._C._cuda_isCurrentStreamCapturing():
+            return  # a graph's replays are no work of this stream
+        now = torch.cuda.current_stream(self.device)
+        for t in (self.k_cache, self.v_cache, self.k_bounds, self._ws):
+            if t is not None:
+                t.record_stream(now)
+        self._streams.add(raw)
 
     def _table(self, page_table, what):
         shape, strides = page_table.shape, page_table.stride()
@@ -201,11 +213,14 @@ class PagedKV:
             return self._on(self.append, stream, k, v, page_table, token_seq, token_pos, q, rope, interleaved, q_out)
         if q is not None and q_out is None:
             q_out = _empty((n, self.n_q_heads, self.head_dim), self._q_strides, self.dtype)
+        raw = _raw_stream(index)
+        if raw not in self._streams:
+            self._first_on(raw)
         rc = _append(layout, n_seqs, n, None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                      None if rope is None else rope.data_ptr(), rope_dim, rope_len, 1 if interleaved else 0,
                      page_table.data_ptr(), token_seq.data_ptr(), token_pos.data_ptr(),
                      None if q is None else q_out.data_ptr(), self._k_at, self._v_at, self._bounds_at, self._status_at,
-                     _raw_stream(index))
+                     raw)
         if rc:
             raise SplitKVError(rc, "splitkv_paged_append")
         return q_out
@@ -231,12 +246,15 @@ class PagedKV:
             return self._on(self.select, stream, q, page_table, seq_lens, n_select, keep_first, keep_last, pages)
         if pages is None:
             pages = _empty(shape, (self.n_kv_heads * n_select, n_select, 1), _I32)
+        raw = _raw_stream(index)
+        if raw not in self._streams:
+            self._first_on(raw)
         # Scratch of the call alone: 8 bytes per page and kv head. No sequence has more pages than its row: any larger
         # number of kept ones says the same.
         ws = _empty((n * self.n_kv_heads * page_table.shape[1] * 2 + 4,), (1,), _I32)
         rc = _select(layout, n, q.data_ptr(), qs, self._bounds_at, page_table.data_ptr(), seq_lens.data_ptr(), n_select,
                      min(int(keep_first), _MOST), min(int(keep_last), _MOST), pages.data_ptr(), self._status_at,
-                     ws.data_ptr(), ws.shape[0] * 4, _raw_stream(index))
+                     ws.data_ptr(), ws.shape[0] * 4, raw)
         if rc:
             raise SplitKVError(rc, "splitkv_paged_select")
         return pages
@@ -270,6 +288,8 @@ class PagedKV:
         if lse is None:
             lse = _empty((n, heads), (heads, 1), _F32)
         raw = _raw_stream(index)
+        if raw not in self._streams:
+            self._first_on(raw)
         args = (layout, n, q.data_ptr(), qs, self._k_at, self._v_at, page_table.data_ptr(), seq_lens.data_ptr(), pages_at,
                 n_select, o.data_ptr(), lse.data_ptr(), self._status_at)
         if torch._C._cuda_isCurrentStreamCapturing():

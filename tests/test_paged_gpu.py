@@ -742,6 +742,45 @@ def test_calls_see_what_the_kernel_before_them_wrote():
         assert all(torch.equal(x.nan_to_num(77.0), y.nan_to_num(77.0)) for x, y in zip(w, g))
 
 
+def _ranges(tensors):
+    return [(t.untyped_storage().data_ptr(), t.untyped_storage().nbytes()) for t in tensors]
+
+
+def _meet(ranges, tensors):
+    return any(p < q + m and q < p + n for p, n in ranges for q, m in _ranges(tensors))
+
+
+@pytest.mark.parametrize("call", ["decode", "select", "append"])
+def test_a_dropped_object_keeps_its_memory_until_its_calls_are_done(call):
+    # Work of a call on another stream than the memory's own is still waiting there when the last reference goes.
+    c = Case([3000], 8, 2, 64, 16)
+    kv = PagedKV(8, 2, 64, 16, max_seqs=1, max_pages=c.table.shape[1], n_pages=c.k.shape[0], bounds=True)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    for t in (kv.k_cache, kv.v_cache, kv.k_bounds):
+        t.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = _ranges([kv.k_cache, kv.v_cache, kv.k_bounds, kv._ws])
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)  # 0.2 s
+        if call == "decode":
+            kv.decode(c.q, c.table, c.lens)
+        elif call == "select":
+            kv.select(c.q, c.table, c.lens, 5)
+        else:
+            kv.append(x, x, c.table, one, one)
+    del kv
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in held]
+    waiting = not side.query()
+    met = _meet(held, others)
+    torch.cuda.synchronize()
+    assert waiting and not met
+    del others
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in held]
+    assert _meet(held, again)  # then it is given back
+
+
 def test_graphs_follow_their_inputs_and_share_nothing():
     # Two graphs of one object, replayed side by side with eager calls between: each keeps its results.
     c = Case([6000, 3000], 32, 4, 128, 16)
