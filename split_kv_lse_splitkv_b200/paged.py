@@ -53,7 +53,8 @@ class PagedKV:
     :meth:`select` only (``bounds=True`` allocates it).
 
     Every call takes a page table (int32 [n_seqs, up to max_pages]: row b lists the pages of sequence b) and is
-    enqueued on the current stream (``stream=``: on that one); none synchronizes (making the object does). Lengths,
+    enqueued on the current stream (``stream=``: on that one, which its tensors then belong to as well: they may be
+    dropped at once; what it returns is that stream's); none synchronizes (making the object does). Lengths,
     tables and token lists are read on the device, so a call captured into a CUDA graph follows their values at each
     replay. The object's scratch is shared by its decode calls: on a change of stream the new one waits for the old
     one, and a captured call has scratch of its own. A stream given by its handle has to outlive the object. Results
@@ -138,7 +139,12 @@ class PagedKV:
             stream = torch.cuda.ExternalStream(int(stream), device=self.device)
         _need(stream.device == self.device, "PagedKV: a stream of another device than the cache's")
         with torch.cuda.stream(stream):
-            return fn(*args)
+            got = fn(*args)
+            if not torch._C._cuda_isCurrentStreamCapturing():
+                for t in args:  # may be dropped as soon as the call returns, and belong to another stream
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(stream)
+            return got
 
     def _first_on(self, raw) -> None:
         """The first call on the current stream. The object may be dropped while work of its calls is under way, on streams

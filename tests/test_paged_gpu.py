@@ -781,6 +781,40 @@ def test_a_dropped_object_keeps_its_memory_until_its_calls_are_done(call):
     assert _meet(held, again)  # then it is given back
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_tensors_of_a_call_on_a_given_stream_may_be_dropped(raw):
+    c = Case([3000], 8, 2, 64, 16)
+    kb = torch.zeros(c.k.shape[0], 2, 2, 64, dtype=BF, device="cuda")
+    kv = PagedKV(8, 2, 64, 16, max_seqs=1, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    rope = rope_table(16, 64)
+    pages = kv.select(c.q, c.table, c.lens, 5)
+    side = torch.cuda.Stream()
+    handle = side.cuda_stream if raw else side
+
+    def fresh(t):
+        return t.clone(memory_format=torch.contiguous_format)
+
+    for call, given in ((lambda a: kv.decode(*a, stream=handle), (c.q, c.table, c.lens, pages)),
+                        (lambda a: kv.decode(*a[:3], o=a[3], lse=a[4], stream=handle),
+                         (c.q, c.table, c.lens, torch.empty_like(c.q), torch.empty(1, 8, device="cuda"))),
+                        (lambda a: kv.select(*a, 5, stream=handle), (c.q, c.table, c.lens)),
+                        (lambda a: kv.append(*a[:5], q=a[5], rope=a[6], stream=handle), (x, x, c.table, one, one, c.q, rope))):
+        given = [fresh(t) for t in given]
+        torch.cuda.synchronize()
+        held, sizes = _ranges(given), [t.untyped_storage().nbytes() for t in given]
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000_000)  # 0.2 s
+        got = call(given)
+        given.clear()
+        others = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+        waiting, met = not side.query(), _meet(held, others)
+        torch.cuda.synchronize()
+        assert waiting and not met
+        del got, others
+
+
 def test_graphs_follow_their_inputs_and_share_nothing():
     # Two graphs of one object, replayed side by side with eager calls between: each keeps its results.
     c = Case([6000, 3000], 32, 4, 128, 16)
