@@ -43,6 +43,26 @@ def _need(ok, what: str) -> None:
         raise SplitKVError(EINVAL, what)
 
 
+# Status words by device index, [words, number taken] each. They are never given back: a captured graph goes on reading
+# and writing the word of an object that is gone.
+_WORDS = 128
+_words = {}
+_words_lock = threading.Lock()
+
+
+def _status_word(device, index) -> torch.Tensor:
+    with _words_lock:
+        blocks = _words.setdefault(index, [])
+        if not blocks or blocks[-1][1] == _WORDS:
+            words = torch.zeros(_WORDS, dtype=_I32, device=device)
+            if device.type == "cuda":
+                torch.cuda.current_stream(device).synchronize()  # the next ones may be taken on another stream
+            blocks.append([words, 0])
+        block = blocks[-1]
+        block[1] += 1
+        return block[0][block[1] - 1:block[1]]
+
+
 class PagedKV:
     """The paged cache of one attention layer and its calls.
 
@@ -58,7 +78,8 @@ class PagedKV:
     tables and token lists are read on the device, so a call captured into a CUDA graph follows their values at each
     replay. The object's scratch is shared by its decode calls: on a change of stream the new one waits for the old
     one, and a captured call has scratch of its own. A stream given by its handle has to outlive the object. Results
-    carry no autograd history. Errors that only the device sees collect in :attr:`status`; while it is not zero, calls
+    carry no autograd history. The object may be dropped while calls are under way; a graph that was captured from it
+    needs the caches and bounds that it was captured with. Errors that only the device sees collect in :attr:`status`; while it is not zero, calls
     do no work (:meth:`check_status` raises; zero it to go on).
     """
 
@@ -102,14 +123,14 @@ class PagedKV:
         self._ws = self._stream = None
         self._streams = set()  # those that _first_on has seen
         if self._index is None:
-            self.status = torch.zeros(1, dtype=_I32, device=self.device)
-        else:  # the status word and the scratch, whose counters start at zero: before any stream's first call
+            self.status = _status_word(self.device, None)
+        else:  # the scratch, whose counters start at zero: before any stream's first call
             if torch.cuda.is_current_stream_capturing():
                 raise SplitKVError(EINVAL, "PagedKV: made during a stream capture")
-            self._ws = torch.empty(16 + self._ws_bytes, dtype=torch.uint8, device=self.device)
-            self._ws[:16 + _COUNTERS].zero_()
-            self.status = self._ws[:4].view(_I32)
-            self._ws_at = self._ws.data_ptr() + 16
+            self.status = _status_word(self.device, self._index)
+            self._ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+            self._ws[:_COUNTERS].zero_()
+            self._ws_at = self._ws.data_ptr()
             self._stream = torch.cuda.current_stream(self.device)
             self._stream.synchronize()
         # The object's own tensors, which it keeps.

@@ -320,3 +320,14 @@ def test_kernels_launched_early_read_through_coherent_loads():
         with open(os.path.join(csrc, name)) as f:
             code = "\n".join(line.split("//")[0] for line in f)
         assert not re.search(r"__ldg|__restrict__|ld\.global\.nc|__constant__", code), name
+
+
+def test_status_words_are_never_given_back():
+    a = make()
+    at = a.status.data_ptr()
+    assert a.status.shape == (1,) and a.status_value() == 0
+    a.status.fill_(3)  # what a graph of its calls may do after it is gone
+    others = [make() for _ in range(3)]
+    assert len({at, *(x.status.data_ptr() for x in others)}) == 4
+    del a
+    assert all(x.status_value() == 0 for x in others + [make() for _ in range(300)])

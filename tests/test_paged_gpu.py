@@ -11,6 +11,7 @@ sums of n terms by n 2^-23 more. So
     |lse - ref| <= e' + n 2^-23 + 2^-23 |ref|.
 Rotations: two products and a sum in float32 (3 roundings of 2^-24 on |x| + |y|), then one rounding to the type.
 """
+import gc
 import threading
 
 import numpy as np
@@ -813,6 +814,35 @@ def test_tensors_of_a_call_on_a_given_stream_may_be_dropped(raw):
         torch.cuda.synchronize()
         assert waiting and not met
         del got, others
+
+
+def test_a_graph_outlives_the_object_it_was_captured_from():
+    # Caches, bounds and outputs are kept, the object is not; what it held is somebody else's by the time of the replay.
+    c = Case([3000, 40], 8, 2, 64, 16)
+    kb = torch.randn(c.k.shape[0], 2, 2, 64, device="cuda").sort(2).values.to(BF)
+    kv = PagedKV(8, 2, 64, 16, max_seqs=2, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    want = [t.clone() for t in (*kv.decode(c.q, c.table, c.lens), kv.select(c.q, c.table, c.lens, 5))]
+    got = [torch.zeros_like(t) for t in want]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.decode(c.q, c.table, c.lens, o=got[0], lse=got[1])
+        kv.select(c.q, c.table, c.lens, 5, pages=got[2])
+    size = kv._ws.numel()
+    del kv
+    gc.collect()
+    taken = [torch.full((n,), -1, dtype=torch.int32, device="cuda") for n in [size // 4 + 4, size // 4] + [4] * 600]
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert all(bool((t == -1).all()) for t in taken)
+
+
+def test_status_words_are_apart():
+    c = Case([64], 4, 2, 64, 16)
+    kvs = [PagedKV(4, 2, 64, 16, max_seqs=1, max_pages=4, k_cache=c.k, v_cache=c.v) for _ in range(140)]
+    assert len({kv.status.data_ptr() for kv in kvs}) == len(kvs)
+    kvs[77].decode(c.q, c.table, c.lens + 1)
+    assert [kv.status_value() for kv in kvs] == [B.DEV_BAD_LENGTH if i == 77 else 0 for i in range(140)]
 
 
 def test_graphs_follow_their_inputs_and_share_nothing():
