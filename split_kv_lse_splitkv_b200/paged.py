@@ -106,7 +106,7 @@ class PagedKV:
             _need(tuple(k_bounds.shape) == (shape[0], shape[1], 2, shape[3]) and k_bounds.is_contiguous() and
                   k_bounds.dtype == k_cache.dtype and k_bounds.device == k_cache.device,
                   "PagedKV: k_bounds must be a dense [n_pages, n_kv_heads, 2, head_dim] tensor of the caches' type")
-        self.k_cache, self.v_cache, self.k_bounds = k_cache, v_cache, k_bounds
+        self._k_cache, self._v_cache, self._k_bounds = k_cache, v_cache, k_bounds
         self.dtype, self.device = k_cache.dtype, k_cache.device
         self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), shape[1], shape[3]
         self.page_size, self.max_seqs, self.max_pages = shape[2], int(max_seqs), int(max_pages)
@@ -123,28 +123,34 @@ class PagedKV:
         self._ws = self._stream = None
         self._streams = set()  # those that _first_on has seen
         if self._index is None:
-            self.status = _status_word(self.device, None)
+            self._status = _status_word(self.device, None)
         else:  # the scratch, whose counters start at zero: before any stream's first call
             if torch.cuda.is_current_stream_capturing():
                 raise SplitKVError(EINVAL, "PagedKV: made during a stream capture")
-            self.status = _status_word(self.device, self._index)
+            self._status = _status_word(self.device, self._index)
             self._ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
             self._ws[:_COUNTERS].zero_()
             self._ws_at = self._ws.data_ptr()
             self._stream = torch.cuda.current_stream(self.device)
             self._stream.synchronize()
         # The object's own tensors, which it keeps.
-        self._k_at, self._v_at, self._status_at = k_cache.data_ptr(), v_cache.data_ptr(), self.status.data_ptr()
+        self._k_at, self._v_at, self._status_at = k_cache.data_ptr(), v_cache.data_ptr(), self._status.data_ptr()
         self._bounds_at = None if k_bounds is None else k_bounds.data_ptr()
+
+    # Read only: the kernels are called with the addresses of these tensors, taken once.
+    k_cache = property(lambda self: self._k_cache)
+    v_cache = property(lambda self: self._v_cache)
+    k_bounds = property(lambda self: self._k_bounds)
+    status = property(lambda self: self._status)
 
     # -- marshalling. These calls are made once per layer and token: checks are plain comparisons, texts are made only where
     # one fails, and the library is called with integers.
     def _layout(self, width: int, stride: int):
         got = self._layouts.get((width, stride))
         if got is None:
-            st = self.k_cache.stride()
+            st = self._k_cache.stride()
             got = ctypes.byref(B.make_paged(self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size,
-                                            self.k_cache.shape[0], width, st[:3], stride, self._scale, self.dtype))
+                                            self._k_cache.shape[0], width, st[:3], stride, self._scale, self.dtype))
             if len(self._layouts) < 64:
                 self._layouts[(width, stride)] = got
         return got
@@ -173,7 +179,7 @@ class PagedKV:
         if torch._C._cuda_isCurrentStreamCapturing():
             return  # a graph's replays are no work of this stream
         now = torch.cuda.current_stream(self.device)
-        for t in (self.k_cache, self.v_cache, self.k_bounds, self._ws):
+        for t in (self._k_cache, self._v_cache, self._k_bounds, self._ws):
             if t is not None:
                 t.record_stream(now)
         self._streams.add(raw)
@@ -257,7 +263,7 @@ class PagedKV:
         the new token of each sequence reads at each kv head, ascending, then -1. The first ``keep_first`` and last
         ``keep_last`` pages are always among them, the others are those with the largest bound on their scores."""
         what = "PagedKV.select"
-        if self.k_bounds is None:
+        if self._k_bounds is None:
             raise SplitKVError(EINVAL, f"{what}: the cache has no bounds (PagedKV(..., bounds=True))")
         n, layout = self._table(page_table, what)
         qs = self._rows(q, n, self.n_q_heads, what, "q")
@@ -350,7 +356,7 @@ class PagedKV:
 
     # -- host-side reads (synchronizing; for tests and reports)
     def status_value(self) -> int:
-        return int(self.status.item())
+        return int(self._status.item())
 
     def check_status(self):
         st = self.status_value()

@@ -331,3 +331,13 @@ def test_status_words_are_never_given_back():
     assert len({at, *(x.status.data_ptr() for x in others)}) == 4
     del a
     assert all(x.status_value() == 0 for x in others + [make() for _ in range(300)])
+
+
+@pytest.mark.parametrize("name", ["k_cache", "v_cache", "k_bounds", "status"])
+def test_the_tensors_of_an_object_are_not_replaced(name):
+    # The kernels are called with the addresses of those it was made with.
+    kv = make()
+    held = getattr(kv, name)
+    with pytest.raises(AttributeError):
+        setattr(kv, name, held.clone())
+    assert getattr(kv, name) is held
