@@ -355,7 +355,8 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
  *                     times with the lengths that each of them sees.
  *   q, o              [n_seqs, Hq, d]; q's tokens are q_stride elements apart (a slice of a fused
  *                     projection), each token's heads dense; o and lse [n_seqs, Hq] are dense.
- * What a call writes lies apart from what it reads, and its outputs from each other (EINVAL where the call can tell).
+ * What a call writes lies apart from what it reads, and its outputs and workspace from each other (EINVAL, but for rows
+ * of the caches: those that no call uses may serve for anything).
  * Pointers are 16-byte aligned and every stride a multiple of 16 bytes (k_cache, v_cache, k_bounds, q, k,
  * v, o, rope and workspaces; lists and tables of int32 need their own alignment only). Sums, maxima and
  * partial results are float32; the choice of pages is that of float64 scores, so that no rounding decides it.

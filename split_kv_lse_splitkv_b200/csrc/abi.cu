@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstring>
 #include <functional>
+#include <initializer_list>
 #include <queue>
 #include <utility>
 #include <vector>
@@ -440,6 +441,7 @@ int build_paged(const splitkv_paged* p, int64_t n_seqs, PagedMeta* m) {
     if (p->n_q_heads < 1 || p->n_kv_heads < 1 || p->n_q_heads % p->n_kv_heads || p->head_dim < 1) return SPLITKV_EINVAL;
     if (p->page_size < 1 || p->n_pages < 1 || p->max_pages < 1 || p->table_stride < p->max_pages) return SPLITKV_EINVAL;
     if (n_seqs < 0) return SPLITKV_EINVAL;
+    if (p->table_stride > (int64_t)1 << 40) return SPLITKV_EUNSUPPORTED;
     if (!(p->scale > 0.f) || p->scale != p->scale || p->scale > 3.0e38f) return SPLITKV_EINVAL;
     if (p->dtype != SPLITKV_F32 && p->dtype != SPLITKV_BF16) return SPLITKV_EUNSUPPORTED;
     const int32_t vec = p->dtype == SPLITKV_BF16 ? 8 : 4;  // elements of 16 bytes
@@ -496,6 +498,26 @@ bool overlap(const void* x, int64_t x_bytes, const void* y, int64_t y_bytes) {
     return (const char*)x < (const char*)y + y_bytes && (const char*)y < (const char*)x + x_bytes;
 }
 
+// Bytes that a call reads or writes; at null: there are none.
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+// Whether something that is written meets something else, read or written: other blocks may still need what was there.
+// The caches are not among them: rows that are not in use may serve for anything.
+bool written_over(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+    for (const Span* w = written.begin(); w != written.end(); ++w) {
+        if (!w->at) continue;
+        for (const Span* x = written.begin(); x != w; ++x)
+            if (x->at && overlap(w->at, w->bytes, x->at, x->bytes)) return true;
+        for (const Span& x : read)
+            if (x.at && overlap(w->at, w->bytes, x.at, x.bytes)) return true;
+    }
+    return false;
+}
+int64_t table_bytes(const PagedMeta& m) { return m.n_seqs ? ((m.n_seqs - 1) * m.table_stride + m.max_pages) * 4 : 0; }
+int64_t bounds_bytes(const PagedMeta& m) { return m.n_pages * m.hkv * 2 * m.d * (m.dtype == SPLITKV_BF16 ? 2 : 4); }
+
 }  // namespace
 
 SPLITKV_API size_t splitkv_paged_workspace_size(const splitkv_paged* paged, int32_t n_seqs) {
@@ -528,13 +550,15 @@ SPLITKV_API int splitkv_paged_append(const splitkv_paged* paged, int32_t n_seqs,
     if (q && (!rows_ok(m, q, n_tokens, q_stride, m.hq) || !q_out || !aligned16(q_out))) return SPLITKV_EINVAL;
     if (!page_table_d || !token_seq_d || !token_pos_d || !k_cache || !v_cache || k_cache == v_cache) return SPLITKV_EINVAL;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_bounds) || !aligned16(rope)) return SPLITKV_EINVAL;
-    if (q) {  // q_out is written while other blocks still read q, k and v
-        const int64_t out = rows_bytes(m, n_tokens, (int64_t)m.hq * m.d, m.hq);
-        if (overlap(q_out, out, q, rows_bytes(m, n_tokens, q_stride, m.hq)) ||
-            overlap(q_out, out, k, rows_bytes(m, n_tokens, k_stride, m.hkv)) ||
-            overlap(q_out, out, v, rows_bytes(m, n_tokens, v_stride, m.hkv)))
-            return SPLITKV_EINVAL;
-    }
+    if (written_over({{q ? q_out : nullptr, rows_bytes(m, n_tokens, (int64_t)m.hq * m.d, m.hq)}, {k_bounds, bounds_bytes(m)}},
+                     {{q, rows_bytes(m, n_tokens, q_stride, m.hq)},
+                      {k, rows_bytes(m, n_tokens, k_stride, m.hkv)},
+                      {v, rows_bytes(m, n_tokens, v_stride, m.hkv)},
+                      {rope, std::min<int64_t>(rope_len, INT32_MAX) * rope_dim * 4},
+                      {page_table_d, table_bytes(m)},
+                      {token_seq_d, n_tokens * 4},
+                      {token_pos_d, n_tokens * 4}}))
+        return SPLITKV_EINVAL;
     const AppendArgs a{n_tokens, q,           k,          v,           q_stride,    k_stride, v_stride,
                        rope,     rope_dim,    interleaved, rope_len,   page_table_d, token_seq_d, token_pos_d,
                        q_out,    k_cache,     v_cache,     k_bounds};
@@ -558,9 +582,13 @@ SPLITKV_API int splitkv_paged_decode(const splitkv_paged* paged, int32_t n_seqs,
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return SPLITKV_EINVAL;
     if (!workspace_d || workspace_bytes < paged_decode_workspace(m)) return SPLITKV_ENOSPACE;
     if (!aligned16(workspace_d)) return SPLITKV_EINVAL;
-    const int64_t q_bytes = rows_bytes(m, n_seqs, q_stride, m.hq), o_bytes = rows_bytes(m, n_seqs, (int64_t)m.hq * m.d, m.hq);
-    const int64_t lse_bytes = (int64_t)n_seqs * m.hq * 4;
-    if (overlap(o, o_bytes, q, q_bytes) || overlap(lse, lse_bytes, q, q_bytes) || overlap(o, o_bytes, lse, lse_bytes))
+    if (written_over({{o, rows_bytes(m, n_seqs, (int64_t)m.hq * m.d, m.hq)},
+                      {lse, (int64_t)n_seqs * m.hq * 4},
+                      {workspace_d, (int64_t)paged_decode_workspace(m)}},
+                     {{q, rows_bytes(m, n_seqs, q_stride, m.hq)},
+                      {page_table_d, table_bytes(m)},
+                      {seq_len_d, (int64_t)n_seqs * 4},
+                      {pages_d, (int64_t)n_seqs * m.hkv * n_select * 4}}))
         return SPLITKV_EINVAL;
     return cuda_status(launch_paged_decode(m, q, q_stride, k_cache, v_cache, page_table_d, seq_len_d, pages_d,
                                            pages_d ? n_select : 0, o, lse, status_d, workspace_d,
@@ -583,6 +611,12 @@ SPLITKV_API int splitkv_paged_select(const splitkv_paged* paged, int32_t n_seqs,
     if (!aligned16(k_bounds)) return SPLITKV_EINVAL;
     if (!workspace_d || workspace_bytes < paged_select_workspace(m)) return SPLITKV_ENOSPACE;
     if (!aligned16(workspace_d)) return SPLITKV_EINVAL;
+    if (written_over({{pages_d, (int64_t)n_seqs * m.hkv * n_select * 4}, {workspace_d, (int64_t)paged_select_workspace(m)}},
+                     {{q, rows_bytes(m, n_seqs, q_stride, m.hq)},
+                      {k_bounds, bounds_bytes(m)},
+                      {page_table_d, table_bytes(m)},
+                      {seq_len_d, (int64_t)n_seqs * 4}}))
+        return SPLITKV_EINVAL;
     return cuda_status(launch_paged_select(m, q, q_stride, k_bounds, page_table_d, seq_len_d, n_select, keep_first,
                                            keep_last, pages_d, status_d, workspace_d, (cudaStream_t)stream));
 }

@@ -169,6 +169,50 @@ def test_decode_outputs_lie_apart():
         assert e.value.code == code, kw
 
 
+def _apart(call, args, over):
+    """Each of `over` = (name, (tensor, first element)) puts one tensor of the call where it may not be."""
+    for name, (at, first) in over:
+        with pytest.raises(B.SplitKVError) as e:
+            call({**args, name: at[first:]})
+        assert e.value.code == B.EINVAL, name
+
+
+def test_decode_writes_apart_from_lists_and_scratch():
+    # Elements of 4 bytes: q, o 4 x 256, lse 32, lengths 4, table 16 (rows of 4), pages 4 x 2 x 3.
+    f = {k: torch.empty(1 << 16, dtype=torch.int32) for k in ("q", "k_cache", "v_cache", "page_table", "seq_len", "pages", "o", "lse", "status")}
+    n = B.splitkv_paged_workspace_size(desc(), 4) // 4
+    f["workspace"] = torch.empty(n + (1 << 16), dtype=torch.int32)
+    _apart(lambda a: B.splitkv_paged_decode(desc(), 4, **a, q_stride=512, n_select=3, stream=0), f,
+           [("seq_len", (f["o"], 1020)), ("seq_len", (f["lse"], 31)), ("seq_len", (f["workspace"], n - 1)),
+            ("page_table", (f["o"], 1023)), ("page_table", (f["lse"], 0)), ("page_table", (f["workspace"], 300)),
+            ("pages", (f["o"], 1000)), ("pages", (f["lse"], 30)), ("pages", (f["workspace"], 0)),
+            ("lse", (f["pages"], 23)), ("lse", (f["page_table"], 15)), ("lse", (f["seq_len"], 3)),
+            ("o", (f["workspace"], 64)), ("lse", (f["workspace"], n - 1)), ("q", (f["workspace"], 128))])
+
+
+def test_select_writes_apart_from_what_it_reads():
+    # Pages 4 x 2 x 3, scratch 4 x 2 x 4 x 2, bounds 10 x 2 x 64 x 2 / 2.
+    f = {k: torch.empty(1 << 16, dtype=torch.int32) for k in ("q", "k_bounds", "page_table", "seq_len", "pages", "status", "workspace")}
+    _apart(lambda a: B.splitkv_paged_select(desc(), 4, **a, q_stride=512, n_select=3, keep_first=1, keep_last=1, stream=0), f,
+           [("pages", (f["workspace"], 63)), ("pages", (f["seq_len"], 3)), ("pages", (f["page_table"], 15)),
+            ("pages", (f["q"], 1023)), ("pages", (f["k_bounds"], 1279)), ("seq_len", (f["pages"], 23)),
+            ("workspace", (f["pages"], 20)), ("seq_len", (f["workspace"], 60)), ("q", (f["workspace"], 60)),
+            ("page_table", (f["workspace"], 63)), ("k_bounds", (f["workspace"], 60))])
+
+
+def test_append_writes_apart_from_what_it_reads():
+    # Five tokens: q_out 5 x 256, k and v 5 x 64, bounds 1280, a rope table of 100 x 64.
+    f = {k: torch.empty(1 << 16, dtype=torch.int32)
+         for k in ("q", "k", "v", "rope", "page_table", "token_seq", "token_pos", "q_out", "k_cache", "v_cache", "k_bounds", "status")}
+    _apart(lambda a: B.splitkv_paged_append(desc(), 4, 5, **a, q_stride=512, k_stride=128, v_stride=128, rope_dim=64, rope_len=100,
+                                            interleaved=0, stream=0), f,
+           [("rope", (f["q_out"], 1276)), ("page_table", (f["q_out"], 1279)), ("token_seq", (f["q_out"], 1279)),
+            ("token_pos", (f["q_out"], 5)), ("k_bounds", (f["q_out"], 1276)), ("q_out", (f["k_bounds"], 1276)),
+            ("k", (f["k_bounds"], 1276)), ("v", (f["k_bounds"], 0)), ("q", (f["k_bounds"], 64)), ("rope", (f["k_bounds"], 64)),
+            ("token_seq", (f["k_bounds"], 9)), ("token_pos", (f["k_bounds"], 1279)), ("page_table", (f["k_bounds"], 1279)),
+            ("k_bounds", (f["rope"], 6396)), ("q_out", (f["token_pos"], 4))])
+
+
 def test_append_caches_lie_apart():
     f = [torch.empty(1 << 16, dtype=torch.int32) for _ in range(6)]
     with pytest.raises(B.SplitKVError) as e:
