@@ -368,7 +368,9 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
  * nothing outside the given buffers is read or written.
  */
 
-/* Most sequences one call may hold, and most pages of a sequence that splitkv_paged_select ranks. */
+/* Most sequences one call may hold, and most pages of a sequence that splitkv_paged_select ranks. splitkv_paged_decode
+ * further wants (ceil(max_pages * page_size / 16) + 4) * Hkv * ceil(Hq / Hkv / 8) < 2^31 (EUNSUPPORTED; its workspace
+ * query says 0): 16 kv heads at rows of the most positions, 2047 at 2^24. */
 #define SPLITKV_PAGED_MAX_SEQS 4096
 #define SPLITKV_PAGED_MAX_SELECT_PAGES 131072
 

@@ -450,10 +450,6 @@ int build_paged(const splitkv_paged* p, int64_t n_seqs, PagedMeta* m) {
     // Positions, rounded up to a page and a tile, in 31 bits.
     if (p->n_pages > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX - 2048) return SPLITKV_EUNSUPPORTED;
     if (n_seqs > SPLITKV_PAGED_MAX_SEQS || p->n_q_heads > 32768) return SPLITKV_EUNSUPPORTED;
-    // The units of work (16 positions of a sequence, kv head and 8 query rows) are counted in 31 bits.
-    if (n_seqs * (((int64_t)p->max_pages * p->page_size + 15) / 16 + 4) >
-        INT32_MAX / ((int64_t)p->n_kv_heads * ((p->n_q_heads / p->n_kv_heads + 7) / 8)))
-        return SPLITKV_EUNSUPPORTED;
     if (p->page_stride % vec || p->head_stride % vec || p->token_stride % vec) return SPLITKV_EINVAL;
     // No two rows of the cache may overlap: by ascending stride, each step goes past what the smaller ones cover.
     std::pair<int64_t, int64_t> dim[3] = {
@@ -522,7 +518,7 @@ int64_t bounds_bytes(const PagedMeta& m) { return m.n_pages * m.hkv * 2 * m.d * 
 
 SPLITKV_API size_t splitkv_paged_workspace_size(const splitkv_paged* paged, int32_t n_seqs) {
     PagedMeta m;
-    return build_paged(paged, n_seqs, &m) ? 0 : paged_decode_workspace(m);
+    return build_paged(paged, n_seqs, &m) || paged_decode_units(m) > INT32_MAX ? 0 : paged_decode_workspace(m);
 }
 
 SPLITKV_API size_t splitkv_paged_select_workspace_size(const splitkv_paged* paged, int32_t n_seqs) {
@@ -574,6 +570,7 @@ SPLITKV_API int splitkv_paged_decode(const splitkv_paged* paged, int32_t n_seqs,
     PagedMeta m;
     int rc = build_paged(paged, n_seqs, &m);
     if (rc) return rc;
+    if (paged_decode_units(m) > INT32_MAX) return SPLITKV_EUNSUPPORTED;
     if (!status_d || (pages_d && n_select < 1)) return SPLITKV_EINVAL;
     if (pages_d && n_select > (1 << 30) / m.hkv) return SPLITKV_EUNSUPPORTED;
     if (n_seqs == 0) return SPLITKV_OK;

@@ -46,6 +46,9 @@ cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_str
                                 const int32_t* pages, int32_t n_select, void* o, float* lse, int32_t* status, void* ws,
                                 cudaStream_t st);
 size_t paged_decode_workspace(const PagedMeta& m);
+// The most units of work (16 positions at a kv head and 8 query rows) that one sequence may have. A launch counts its
+// sequences' in 31 bits; a call makes as many launches as that takes.
+int64_t paged_decode_units(const PagedMeta& m);
 
 cudaError_t launch_paged_select(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_bounds,
                                 const int32_t* table, const int32_t* seq_len, int32_t n_select, int32_t keep_first,

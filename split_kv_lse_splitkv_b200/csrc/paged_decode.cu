@@ -351,7 +351,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
 }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 
-// The line of units (fewer than 2^31: the entry point sees to it). A segment (sequence, kv head, group of query rows)
+// The line of units (fewer than 2^31: the launch sees to it). A segment (sequence, kv head, group of query rows)
 // takes kSegmentCost units before its tiles': what it costs to begin one (table, queries, first keys: one after the
 // other) next to the streaming of a tile.
 struct Line {
@@ -870,10 +870,16 @@ size_t paged_decode_workspace(const PagedMeta& m) {
     return with_variant(m, 0, false, [](auto v) { return decltype(v)::kWorkspace; });
 }
 
-cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,
-                                const void* v_cache, const int32_t* table, const int32_t* seq_len,
-                                const int32_t* pages, int32_t n_select, void* o, float* lse, int32_t* status, void* ws,
-                                cudaStream_t st) {
+int64_t paged_decode_units(const PagedMeta& m) {
+    const int64_t tiles = ((int64_t)m.max_pages * m.page + kTile - 1) / kTile;
+    return (tiles + kSegmentCost) * m.hkv * ((m.group + 7) / 8);
+}
+
+namespace {
+
+cudaError_t launch_some(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                        const int32_t* table, const int32_t* seq_len, const int32_t* pages, int32_t n_select, void* o,
+                        float* lse, int32_t* status, void* ws, cudaStream_t st) {
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
@@ -893,6 +899,26 @@ cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_str
                                             lse, status, (uint32_t*)ws, (char*)ws + kCounterBytes),
                           "paged decode");
     });
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedMeta& m, const void* q, int64_t q_stride, const void* k_cache,
+                                const void* v_cache, const int32_t* table, const int32_t* seq_len,
+                                const int32_t* pages, int32_t n_select, void* o, float* lse, int32_t* status, void* ws,
+                                cudaStream_t st) {
+    const int32_t most = (int32_t)(INT32_MAX / paged_decode_units(m));
+    const int64_t size = m.dtype == SPLITKV_BF16 ? 2 : 4;
+    for (int32_t b = 0; b < m.n_seqs; b += most) {
+        PagedMeta some = m;
+        some.n_seqs = std::min(most, m.n_seqs - b);
+        const cudaError_t e =
+            launch_some(some, (const char*)q + b * q_stride * size, q_stride, k_cache, v_cache, table + b * m.table_stride,
+                        seq_len + b, pages ? pages + (int64_t)b * m.hkv * n_select : nullptr, n_select,
+                        (char*)o + (int64_t)b * m.hq * m.d * size, lse + (int64_t)b * m.hq, status, ws, st);
+        if (e != cudaSuccess || most >= m.n_seqs - b) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace splitkv

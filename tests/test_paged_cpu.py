@@ -120,6 +120,23 @@ def test_bad_descriptions_are_refused(kw, code):
     assert e.value.code == code
 
 
+def test_work_that_a_call_may_hold():
+    # 4096 sequences of up to a million positions at 8 kv heads; and what one sequence alone is too much for.
+    many = desc(n_q_heads=8, n_kv_heads=8, page_size=64, max_pages=16384, strides=(8 * 64 * 64, 64 * 64, 64))
+    assert B.splitkv_paged_workspace_size(many, B.PAGED_MAX_SEQS) > 0
+    kv = make(n_kv_heads=8, page_size=64, max_pages=16384, max_seqs=B.PAGED_MAX_SEQS)
+    assert kv.max_seqs == B.PAGED_MAX_SEQS
+    f = torch.empty(64, dtype=torch.int32)
+    for pages, heads, fits in ((1 << 21, 16, True), (1 << 21, 17, False), (1 << 14, 2048, True), (1 << 14, 2049, False)):
+        p = desc(n_q_heads=heads, n_kv_heads=heads, head_dim=8, page_size=1024, max_pages=pages - 3, table_stride=1 << 22,
+                 strides=(heads * 1024 * 8, 1024 * 8, 8))
+        assert (B.splitkv_paged_workspace_size(p, 1) > 0) == fits
+        if not fits:
+            with pytest.raises(B.SplitKVError) as e:
+                B.splitkv_paged_decode(p, 1, f, 8 * heads, f, f, f, f, None, 0, f, f, f, f, stream=0)
+            assert e.value.code == B.EUNSUPPORTED
+
+
 def test_layouts_that_are_accepted():
     for kw in (dict(), dict(strides=(2 * 16 * 64, 64, 128)),               # [pages, positions, heads, d]
                dict(strides=(16 * 64, 10 * 16 * 64, 64)),                  # [heads, pages, positions, d]

@@ -248,6 +248,20 @@ def test_decode_wide_tables(dtype, hq, hkv, d):
 
 # ------------------------------------------------------------------ decode over listed pages
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode_in_several_launches(dtype):
+    # Rows of 2^31 positions at 8 kv heads: two sequences a launch.
+    c = Case([3000, 0, 17, 5000, 1], 16, 8, 64, 1024, dtype, width=(1 << 21) - 3, q_gap=1)
+    c.check(*c.kv.decode(c.q, c.table, c.lens), c.oracle())
+    pages = torch.full((5, 8, 2), -1, dtype=torch.int32)
+    pages[0] = torch.tensor([0, 2])
+    pages[2, :, 0], pages[4, :, 0] = 0, 0
+    pages[3] = torch.tensor([1, 4])
+    pages[3, 5] = torch.tensor([3, -1])
+    c.check(*c.kv.decode(c.q, c.table, c.lens, pages=pages.cuda()), c.oracle(pages=pages.numpy()))
+    c.kv.check_status()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("page", [4, 16, 32])
 def test_decode_listed_pages(dtype, page):
     c = Case([0, 1, 5 * page, 7 * page + 3, 40 * page - 1], 8, 2, 64, page, dtype)
