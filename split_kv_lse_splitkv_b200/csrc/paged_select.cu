@@ -169,7 +169,13 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* q
         const T* head = bounds + (int64_t)g * 2 * m.d;
         uint2* out = scores + ((int64_t)b * m.hkv + g) * m.max_pages;
 
-        auto entry = [&](int32_t p) { return lane < kStep && p + lane < p_end ? paged_page(m, trow, p + lane, status) : -1; };
+        // Page-table entry p + lane, -1 for pages that are not ranked: those that are kept are not read either, as what their
+        // bounds hold would widen the others' error bound (one that is not finite: to all pages of the row).
+        auto entry = [&](int32_t p) {
+            if (lane >= kStep || p + lane >= p_end) return -1;
+            const int32_t page = paged_page(m, trow, p + lane, status);
+            return p + lane < keep_first || p + lane >= count - keep_last ? -1 : page;
+        };
         // Asynchronous copies into a ring of rounds in shared memory: two rounds are on their way while one is summed. (Loads
         // into registers one round ahead left the warps waiting for most of the time: 12 bytes a clock and SM.) A lane
         // reads back what it copied itself, so nothing has to be synchronised.
@@ -260,10 +266,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(PagedMeta m, const T* q
             }
             const int v = sub / (LP / kV), at_p = p + v * kPer + at;
             const int32_t page = __shfl_sync(0xffffffffu, ids[0], (v * kPer + at) & 31);
-            if (sub % (LP / kV) == 0 && at_p < p_end) {
-                const bool kept = at_p < keep_first || at_p >= count - keep_last;
-                out[at_p] = make_uint2(kept || page < 0 ? 0 : score_key(s[0]), 0);
-            }
+            if (sub % (LP / kV) == 0 && at_p < p_end) out[at_p] = make_uint2(page < 0 ? 0 : score_key(s[0]), 0);
             if ((p += kStep) >= p_end) break;
 #pragma unroll
             for (int r = 0; r < kStages; ++r) ids[r] = ids[r + 1];

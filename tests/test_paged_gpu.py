@@ -677,6 +677,36 @@ def test_select_far_scores_and_nan():
         assert got == sorted(order[:m]), m
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 1e4])
+def test_select_bounds_of_kept_pages_do_not_count(dtype, value):
+    # Pages that are taken anyway hold what makes a score say nothing: the others are chosen as without them, and from their
+    # float32 scores (the second word of a page's score is set for one page of a warp's share only; scored again in float64,
+    # all of them hold other things).
+    count, d, hkv, hq, n_select = 4096, 128, 2, 8, 64
+    g = torch.Generator().manual_seed(5)
+    kb = torch.randn(count, hkv, 2, d, generator=g).sort(2).values.to(dtype).cuda()
+    table = torch.randperm(count, generator=g).to(torch.int32)[None].cuda()
+    q = torch.randn(1, hq, d, generator=g).to(dtype).cuda()
+    up, down = (x.sum(1) for x in (lambda y: (np.maximum(y, 0), np.minimum(y, 0)))(f64(q)[0].reshape(hkv, -1, d)))
+    bn = f64(kb)[table[0].cpu().numpy()]
+    for p in (0, 1, count - 3, count - 2, count - 1):
+        kb[table[0, p].long()] = value
+    k = torch.zeros(count, hkv, 1, d, dtype=dtype, device="cuda")
+    paged = B.make_paged(hq, hkv, d, 1, count, count, k.stride()[:3], dtype=dtype)
+    ws = torch.zeros(B.splitkv_paged_select_workspace_size(paged, 1) // 4, dtype=torch.int32, device="cuda")
+    pages = torch.empty(1, hkv, n_select, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.splitkv_paged_select(paged, 1, q, hq * d, kb, table, torch.tensor([count], dtype=torch.int32).cuda(), n_select, 2, 3,
+                           pages, status, ws)
+    assert int(status) == 0
+    for h in range(hkv):
+        s = bn[:, h, 1] @ up[h] + bn[:, h, 0] @ down[h]
+        s[:2], s[-3:] = np.inf, np.inf
+        assert pages[0, h].tolist() == sorted(np.argsort(-s, kind="stable")[:n_select].tolist())
+    assert int((ws.view(hkv, count, 2)[:, :, 1] != 0).sum()) <= hkv * count // 4
+
+
 def test_select_bad_pages_and_lengths():
     c = Case([64, 64], 4, 2, 64, 16)
     kb = torch.zeros(c.k.shape[0], 2, 2, 64, dtype=BF, device="cuda")
