@@ -641,20 +641,22 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(PagedMeta m, Append
 template <typename V>
 cudaError_t launch_pieces(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
     using T = typename V::T;
-    constexpr int kSms = 148;
+    int sms = 0;
+    const cudaError_t known = sm_count(&sms);
+    if (known != cudaSuccess) return known;
     const int rows = 32 / (a.rope_dim / 2 / V::kN + ((m.d - a.rope_dim) / V::kN + 1) / 2);
     const int64_t units = (a.q ? Units(m.hq, 4 * rows).of(a.n_tokens) : 0) + Units(m.hkv, 2 * rows).of(a.n_tokens);
     const int64_t row_blocks = (units + kWarps - 1) / kWarps;
     // Tokens that are looked through for pages at a time: few where each may be a page of its own (1000 sequences' tokens,
     // 32/8 heads: 32 at a time 70 us, so 18), many where there are enough warps.
     const int32_t heads = a.k_bounds ? m.hkv : 1;
-    const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens * heads / (kSms * 16)));
+    const int32_t slice = (int32_t)std::min<int64_t>(32, std::max<int64_t>(1, a.n_tokens * heads / (sms * 16)));
     const int64_t slices = (a.n_tokens + slice - 1) / slice * heads;
     // One launch or two. 32/4 heads, d 128, bf16: 1 token 4.8 us and 5.1, 251 tokens, 32/8 heads (3012 warps' rows) 10.9 and
     // 11.6; 400 tokens of a sequence in pages of 64 (4000) 12.6 and 8.4, 16000 tokens 92 and 74.
-    if (a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv) / rows < kSms * 24) {
+    if (a.n_tokens * ((a.q ? m.hq : 0) + 2 * m.hkv) / rows < sms * 24) {
         // A page is shared by a block's warps where it is long (one token, pages of 128: 4.9 us, by one warp 6.0; of 1024: 12.5, 35.5).
-        const int32_t split = a.k_bounds && m.page > 16 && slices <= kSms * 8 ? kWarps : 1;
+        const int32_t split = a.k_bounds && m.page > 16 && slices <= sms * 8 ? kWarps : 1;
         const int64_t check_blocks = (slices * split + kWarps - 1) / kWarps;
         return note_error(launch_overlapped(append_kernel<V>, check_blocks + row_blocks, kThreads, 0, st, m, a, status,
                                             check_blocks, slice, split),
