@@ -303,6 +303,8 @@ def make_paged(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, s
     if code is None:
         raise SplitKVError(EUNSUPPORTED, f"dtype {dtype}")
     scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
+    if any(abs(int(x)) >= 1 << 31 for x in (n_q_heads, n_kv_heads, head_dim, page_size, max_pages)):
+        raise SplitKVError(EUNSUPPORTED, "make_paged: a size past 31 bits")  # ctypes would cut it off
     return Paged(int(n_q_heads), int(n_kv_heads), int(head_dim), int(page_size), int(n_pages), int(max_pages),
                  int(max_pages if table_stride is None else table_stride), int(strides[0]), int(strides[1]),
                  int(strides[2]), float(scale), code)

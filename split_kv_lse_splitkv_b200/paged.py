@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .binding import EINVAL, SplitKVError
+from .binding import EINVAL, EUNSUPPORTED, SplitKVError
 
 _COUNTERS = 1024  # bytes at the head of the workspace that have to be zero before its first use
 _MOST = (1 << 31) - 1
@@ -271,6 +271,8 @@ class PagedKV:
         n_select = int(n_select)
         if n_select < 1 or keep_first < 0 or keep_last < 0:
             raise SplitKVError(EINVAL, f"{what}: n_select, keep_first, keep_last")
+        if n_select > B.PAGED_MAX_SELECT_PAGES:  # before a result of that size is made
+            raise SplitKVError(EUNSUPPORTED, f"{what}: n_select past {B.PAGED_MAX_SELECT_PAGES}")
         shape = (n, self.n_kv_heads, n_select)
         if pages is not None:
             self._out(pages, shape, _I32, what, "pages")
@@ -307,6 +309,8 @@ class PagedKV:
             n_select = pages.shape[2] if pages.dim() == 3 else 0
             if n_select < 1:
                 raise SplitKVError(EINVAL, f"{what}: pages must be [n_seqs, n_kv_heads, n_select]")
+            if n_select > _MOST:
+                raise SplitKVError(EUNSUPPORTED, f"{what}: n_select past 31 bits")
             self._out(pages, (n, self.n_kv_heads, n_select), _I32, what, "pages")
             pages_at = pages.data_ptr()
         if o is not None:

@@ -402,3 +402,18 @@ def test_the_tensors_of_an_object_are_not_replaced(name):
     with pytest.raises(AttributeError):
         setattr(kv, name, held.clone())
     assert getattr(kv, name) is held
+
+
+def test_sizes_past_31_bits_are_not_cut_off():
+    kv = make()
+    for n in (B.PAGED_MAX_SELECT_PAGES + 1, 1 << 31, (1 << 32) + 2):
+        with pytest.raises(B.SplitKVError) as e:
+            kv.select(bf(3, 8, 64), i32(3, 6), i32(3), n)
+        assert e.value.code == B.EUNSUPPORTED
+    for kw in (dict(max_pages=(1 << 32) + 6), dict(n_q_heads=(1 << 32) + 8)):
+        with pytest.raises(B.SplitKVError) as e:
+            make(**kw)
+        assert e.value.code == B.EUNSUPPORTED
+    with pytest.raises(B.SplitKVError) as e:
+        desc(page_size=(1 << 32) + 16)
+    assert e.value.code == B.EUNSUPPORTED
