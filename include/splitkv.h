@@ -359,7 +359,9 @@ int splitkv_attn_bwd_rank(const splitkv_problem *problem, const void *q, const v
  * of the caches: those that no call uses may serve for anything).
  * Pointers are 16-byte aligned and every stride a multiple of 16 bytes (k_cache, v_cache, k_bounds, q, k,
  * v, o, rope and workspaces; lists and tables of int32 need their own alignment only). Sums, maxima and
- * partial results are float32; the choice of pages is that of float64 scores, so that no rounding decides it.
+ * partial results are float32 (in the bf16 decode the weights enter the value product with 17 bits, and that product's sums
+ * are the tensor core's, cut to float32 rather than rounded); the choice of pages is that of float64 scores, so that no
+ * rounding decides it.
  * The kernels are launched so that they may be placed on the SMs while the kernel before them in the
  * stream drains; they touch memory only once it has completed.
  * Lengths, tables and token lists are device data, read by the kernels only: a call captured into a
@@ -423,7 +425,7 @@ int splitkv_paged_append(const splitkv_paged *paged, int32_t n_seqs, int64_t n_t
  * j < seq_len_d[b]:
  *   s_j = scale * q_bh . k_j,  lse_bh = log sum_j exp(s_j) (natural log),  o_bh = sum_j exp(s_j - lse_bh) v_j
  * A row without keys (length 0, or only scores of -inf) gets o = 0, lse = -inf; where an infinite value
- * is read, o may be NaN. Cache positions at or past
+ * is read, o may be NaN, and a score of +inf makes o and lse NaN. Cache positions at or past
  * the length are not read. pages_d NULL: every key. Otherwise pages_d [n_seqs, Hkv, n_select] lists the page-table
  * entries (page p: positions p*page_size ..) to read for (b, g): strictly ascending, within the sequence's
  * pages, the unused tail filled with -1 (anything else: SPLITKV_DEV_BAD_PAGE).
@@ -440,8 +442,9 @@ int splitkv_paged_decode(const splitkv_paged *paged, int32_t n_seqs, const void 
  * which no key of the page exceeds in sum_h q_bh . k. pages_d [n_seqs, Hkv, n_select] receives the n_select pages
  * to read, in ascending order, then -1: the first keep_first and the last keep_last pages of the sequence, then
  * those with the highest scores; equal scores go to the lower page. The sum is formed as on the left, in float64: a
- * bound that is infinite or NaN (0 * inf) may make it NaN, which counts as the lowest score. The first
- * pages go before the last ones where n_select does not hold both. max_pages is at most
+ * bound that is infinite or NaN (0 * inf) may make it NaN, which counts as the lowest score. Where
+ * n_select does not hold keep_first + keep_last pages, the list is cut off at its end: the first pages, then the earliest of
+ * the last ones, so that the newest page, the one with the token's own key, is not read. max_pages is at most
  * SPLITKV_PAGED_MAX_SELECT_PAGES (EUNSUPPORTED beyond). workspace_d: splitkv_paged_select_workspace_size() bytes of
  * scratch (8 per page, kv head and sequence), written before it is read; calls that share it must be ordered.
  */

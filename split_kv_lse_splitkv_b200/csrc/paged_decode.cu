@@ -151,7 +151,10 @@ struct Frag<__nv_bfloat16, DP, NT> {
         }
     }
     // O += P V. P goes in as two bf16 halves (2^-17 together): with one, its rounding would add as much error to the
-    // output as the output's own rounding; the second product costs nothing, the loads bound the kernel.
+    // output as the output's own rounding; the second product costs nothing, the loads bound the kernel. O adds up in the
+    // tensor core, which cuts what its float32 sums do not hold. Products formed apart and added here, as in float32 below,
+    // would change 0.13% of the outputs of 131071 keys by their last bit (0.36% differ from the rounded exact ones, 0.23%
+    // then), none at 32768 keys, and take longer (32768 keys 22.7 us, 24.6 so; 256 x 100 keys 36.5, 41).
     __device__ __forceinline__ void values(const float (&p)[NT][4], int lane) {
         uint32_t b[NT][4];
 #pragma unroll
@@ -842,14 +845,19 @@ struct Variant {
 // units an SM may get, by the shapes; `listed`: of pages in a list. Variants that these choose between differ in warps
 // only, which the scratch does not see.
 //   More than 8 query heads a kv head: 16 rows a warp read K and V once (4 x 60000 keys, 32/2 heads, d 128: 58 us; 8 rows
-//   a warp, the second half from L2: 66 us). float32 has no registers for 16 rows.
+//   a warp, the second half from L2: 66 us). float32 has no registers for 16 rows; at 8 rows and d 128 it spills 60 bytes.
 //   Warps: as many as leave the registers for a tile of K and of V in flight (d 64, 8 rows: 12 warps 51 us, 16 warps
-//   of fewer registers 57 us; 16 rows: 12 warps 36 us, 8 warps 40 us. d 128, 16 rows: 8 warps 58 us, 10 spill, 96 us).
-//   Where there is little to read, 8: fewer parts to join, no spills (d 128, 4 kv heads: 1000 keys 13.1 us with 12
+//   of fewer registers 57 us; 16 rows: 12 warps 36 us, 8 warps 40 us. d 128, 16 rows: 8 warps, which spill
+//   24 bytes, 58 us, 10 spill more, 96 us).
+//   Where there is little to read, 8, if there is a choice (up to 8 rows, bf16 d 128 and float32 d 64): fewer parts to join,
+//   no spills (d 128, 4 kv heads: 1000 keys 13.1 us with 12
 //   warps, 11.7 with 8; 32768 keys, 55 units an SM, 23.9 and 22.5; 2 x 60000 keys, 203, 50.0 and 49.8; 8 x 131071, 1771,
 //   322 and 330. float32, d 64, 4 kv heads: 27 units 17.6 and 16.7; 55, 27.4 and 27.9; 101, 38.5 and 41.6). A list of pages
 //   is one more load to wait for, which more warps hide (select and decode of 200 pages of 16 positions, 4 kv heads: 43
 //   units 43.6 us with 12 warps, 42.4 with 8; 86, 60.1 and 59.8; 173, 84 and 89).
+// "Little to read" goes by the table's width, as lengths are device data: a table that is far wider than its sequences are
+// long gets 12 warps for them (1000 keys, 4 kv heads: 11.3 us with a table of 63 or 4096 pages, 12.8 with 65536; 333 keys
+// 9.9 and 10.9; 8 x 1000 keys, 8 kv heads, 18.4 and 20.0 from 4096 pages on).
 constexpr int64_t kFewBf16 = 400, kFewBf16Listed = 80, kFewF32 = 40;
 
 template <typename F>

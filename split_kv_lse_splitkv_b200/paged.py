@@ -79,8 +79,9 @@ class PagedKV:
     replay. The object's scratch is shared by its decode calls: on a change of stream the new one waits for the old
     one, and a captured call has scratch of its own. A stream given by its handle has to outlive the object. Results
     carry no autograd history. The object may be dropped while calls are under way; a graph that was captured from it
-    needs the caches and bounds that it was captured with. Errors that only the device sees collect in :attr:`status`; while it is not zero, calls
-    do no work (:meth:`check_status` raises; zero it to go on).
+    needs the caches and bounds that it was captured with. Errors that only the device sees collect in :attr:`status`;
+    while it is not zero, calls do no work and what they return is not written (:meth:`check_status` raises; zero it to
+    go on).
     """
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, page_size, max_seqs, max_pages, n_pages=None, dtype=None,
@@ -261,7 +262,9 @@ class PagedKV:
     def select(self, q, page_table, seq_lens, n_select, keep_first=1, keep_last=1, pages=None, stream=None):
         """int32 [n_seqs, n_kv_heads, n_select]: the pages (indices into the sequence's row of ``page_table``) that
         the new token of each sequence reads at each kv head, ascending, then -1. The first ``keep_first`` and last
-        ``keep_last`` pages are always among them, the others are those with the largest bound on their scores."""
+        ``keep_last`` pages are always among them, the others are those with the largest bound on their scores. An
+        ``n_select`` below ``keep_first + keep_last`` cuts the kept ones off at their end: the newest page, which holds the
+        token's own key, is the first to be left out."""
         what = "PagedKV.select"
         if self._k_bounds is None:
             raise SplitKVError(EINVAL, f"{what}: the cache has no bounds (PagedKV(..., bounds=True))")
