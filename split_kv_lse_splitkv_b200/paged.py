@@ -54,7 +54,8 @@ def _status_word(device, index) -> torch.Tensor:
     with _words_lock:
         blocks = _words.setdefault(index, [])
         if not blocks or blocks[-1][1] == _WORDS:
-            words = torch.zeros(_WORDS, dtype=_I32, device=device)
+            with torch.inference_mode(False):  # objects made outside of that mode share them
+                words = torch.zeros(_WORDS, dtype=_I32, device=device)
             if device.type == "cuda":
                 torch.cuda.current_stream(device).synchronize()  # the next ones may be taken on another stream
             blocks.append([words, 0])

@@ -417,3 +417,12 @@ def test_sizes_past_31_bits_are_not_cut_off():
     with pytest.raises(B.SplitKVError) as e:
         desc(page_size=(1 << 32) + 16)
     assert e.value.code == B.EUNSUPPORTED
+
+
+def test_status_words_of_objects_made_in_inference_mode():
+    with torch.inference_mode():
+        kvs = [make() for _ in range(130)]  # a block of words and more
+        kvs[0].status.fill_(1)
+    for kv in kvs + [make()]:
+        kv.status.zero_()
+        assert kv.status_value() == 0
