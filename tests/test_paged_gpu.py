@@ -919,6 +919,47 @@ def test_graphs_follow_their_inputs_and_share_nothing():
     c.kv.check_status()
 
 
+def test_a_graph_of_several_streams():
+    # One capture: an append, then attention over all keys and over chosen pages side by side, then the next append.
+    c = Case([2000, 700, 1], 8, 2, 64, 16)
+    kb = torch.randn(c.k.shape[0], 2, 2, 64, device="cuda").sort(2).values.to(BF)
+    kv = PagedKV(8, 2, 64, 16, max_seqs=3, max_pages=c.table.shape[1], k_cache=c.k, v_cache=c.v, k_bounds=kb)
+    seq = torch.arange(3, dtype=torch.int32, device="cuda")
+    new = torch.randn(4, 3, 2, 64, device="cuda").to(BF)
+    side = torch.cuda.Stream()
+
+    def run(fork):
+        got = []
+        for x in new:
+            main = torch.cuda.current_stream()
+            kv.append(x, x, c.table, seq, c.lens - 1)
+            if fork:
+                side.wait_stream(main)
+            with torch.cuda.stream(side if fork else main):
+                pages = kv.select(c.q, c.table, c.lens, 9)
+                sparse = kv.decode(c.q, c.table, c.lens, pages=pages)
+            got += [*kv.decode(c.q, c.table, c.lens), pages, *sparse]
+            if fork:
+                main.wait_stream(side)
+        return got
+
+    want = [t.clone() for t in run(False)]
+    state = [t.clone() for t in (c.k, c.v, kb)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(True)
+    for t in (c.k[c.table[0, 0].long()], c.v[c.table[0, 0].long()]):
+        assert not t.isnan().any()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert all(torch.equal(x.nan_to_num(77.0), y.nan_to_num(77.0)) for x, y in zip((c.k, c.v, kb), state))
+    kv.check_status()
+
+
 def test_threads_share_one_object():
     # Each thread on a stream of its own: decode, select and decode over the list, all on one object.
     c = Case([9000, 50, 0, 700], 8, 2, 64, 16)
