@@ -80,7 +80,7 @@ class PagedKV:
     replay. The object's scratch is shared by its decode calls: on a change of stream the new one waits for the old
     one, and a captured call has scratch of its own. A stream given by its handle has to outlive the object. Results
     carry no autograd history. The object may be dropped while calls are under way; a graph that was captured from it
-    needs the caches and bounds that it was captured with. Errors that only the device sees collect in :attr:`status`;
+    needs the caches and bounds that it was captured with until its last replay is done. Errors that only the device sees collect in :attr:`status`;
     while it is not zero, calls do no work and what they return is not written (:meth:`check_status` raises; zero it to
     go on).
     """
