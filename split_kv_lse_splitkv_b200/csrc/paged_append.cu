@@ -670,7 +670,7 @@ cudaError_t launch_pieces(const PagedMeta& m, const AppendArgs& a, int32_t* stat
 }
 
 // 16 bytes a piece where half of rope_dim is a multiple of them, 8 where it is of those (16000 tokens, 32/4 heads, d 80,
-// rope_dim 40 in bf16: 63 us; rope_dim 80, 16 bytes: 53; channel by channel: 196), else channel by channel.
+// rope_dim 40 in bf16: 65 us; rope_dim 80, 16 bytes: 54; rope_dim 20, channel by channel: 188), else channel by channel.
 template <typename T>
 cudaError_t launch(const PagedMeta& m, const AppendArgs& a, int32_t* status, cudaStream_t st) {
     const int half = a.rope_dim / 2;

@@ -28,7 +28,7 @@ constexpr int kLoads = 8;         // copies of 16 bytes of bounds a lane makes i
 constexpr int kStages = 3;        // rounds in flight and in use
 constexpr int kRing = kWarps * kStages * kLoads * 32;  // 16-byte pieces: 192 KB
 // Scores that the second kernel keeps in shared memory (192 KB, or 92 where two blocks share an SM); longer rows stay in L2. 8
-// rows of 18750 pages: 36 us so, from L2 50; 16 rows of 43750: 111, 145.
+// rows of 18750 pages: 36 us so, from L2 50; 16 rows of 43750: 112, 146.
 template <int kPerSm>
 constexpr int kInShared = kPerSm == 1 ? 49152 : 23552;
 constexpr int kCands = 512;       // pages that are ranked one by one
@@ -536,8 +536,8 @@ __device__ __forceinline__ float error_of(const PagedMeta& m) { return (32 + 2 *
 // One block per (sequence, kv head). It runs once through code that nothing has run before, so what counts is how many
 // instructions it has to fetch: loops stay loops. One block an SM (kPerSm = 1) has the registers that it needs (124, no
 // spills; 104 bytes of stack, pick_wide's call among them); two have 64, with 24 to 40 bytes of spills. More rows than SMs
-// want two there. 8 rows of 4096 pages, select as a whole: 13.7 us, 15.9 with two; 2048 rows of 250:
-// 118 us, 98 with two.
+// want two there. 8 rows of 4096 pages, select as a whole: 14.2 us, 16.2 with two; 2048 rows of 250:
+// 115 us, 94 with two.
 template <typename T, int kPerSm>
 __global__ void __launch_bounds__(kThreads, kPerSm) pick_kernel(PagedMeta m, const T* q, int64_t q_stride,
                                                                 const T* bounds, const int32_t* table,
